@@ -45,7 +45,7 @@ def listed():
         dict(name="dispatch_prefill", op="sort", tokens=8192, experts=128, top_k=8, width=4096, dropped=0.0),
         # the gradient of the way back and of the way there, some slots dropped by a capacity limit
         dict(name="combine_grad", op="unsort", tokens=4096, experts=128, top_k=8, width=7168, dropped=0.02),
-        # a prompt's activations quantised while they are gathered into expert order
+        # a prompt's activations quantised on their way into expert order
         dict(name="quantize_rows", op="quantize", tokens=8192, experts=128, top_k=8, width=4096),
         # a training step's weights quantised for the product and, transposed, for its gradient
         dict(name="quantize_weights", op="weights", experts=8, rows=4096, width=7168),
@@ -391,7 +391,7 @@ def _calls(s):
         mxg.mx_moe_permute_backward(s["drows"], row_of_slot, s["dx"])
         return dict(dy=s["dy"], dweights=s["dweights"], dx=s["dx"])
     if op == "quantize":
-        mxg.mx_grouped_quantize_block128_gather(s["x"], s["plan"][2], c["top_k"], s["q"], s["scales"], s["plan"][0])
+        mxg.mx_grouped_quantize_block128_scatter(s["x"], s["plan"][1], s["q"], s["scales"], s["plan"][0])
         return dict(q=s["q"].view(torch.float8_e4m3fn), scales=s["scales"])
     if op == "weights":
         mxg.mx_quantize_weights_block128(s["w"], s["q"], s["scales"], s["q_t"], s["scales_t"])
