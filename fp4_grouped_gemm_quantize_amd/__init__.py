@@ -10,7 +10,16 @@ Entry points (same names as the C ABI in include/mxg.h):
     mx_grouped_matmul_swiglu(fmt, a_q, a_scales, w_q, w_scales, y_q, y_scales, row_offsets, expert_ids,
                              max_rows_per_group_hint=0)
     mx_silu_quantize(h, y_q, y_scales, row_offsets)
-plus allocating conveniences quantize(), grouped_matmul(), grouped_matmul_swiglu(), silu_quantize().
+    mx_moe_topk(score, logits, topk_ids, topk_weights, bias=None, renormalize=True, scale=1.0)
+    mx_moe_sort(topk_ids, row_offsets, row_of_slot, slot_of_row)
+    mx_moe_permute(x, row_of_slot, rows)
+    mx_grouped_quantize_block128(x, q, scales, row_offsets)
+    mx_grouped_matmul_block128(a_q, a_scales, b_q, b_scales, c, row_offsets, expert_ids, max_rows_per_group_hint=0)
+    mx_silu_quantize_block128(h, y_q, y_scales, row_offsets)
+and the gradients mx_moe_topk_backward, mx_moe_permute_backward, mx_moe_combine_backward, mx_silu_backward_block128;
+plus allocating conveniences quantize(), grouped_matmul(), grouped_matmul_swiglu(), silu_quantize(), moe_topk(),
+moe_sort(), moe_permute(), quantize_block128(), quantize_weights_block128(), grouped_matmul_block128(),
+silu_quantize_block128().
 """
 from __future__ import annotations
 
@@ -24,6 +33,9 @@ MXFP8 = 1
 MXFP4 = 2
 FORMATS = {FP8_ROWWISE: "fp8_e4m3_rowwise", MXFP8: "mxfp8_e4m3", MXFP4: "mxfp4_e2m1"}
 
+F32, BF16 = 0, 1                       # mxg_dtype
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1    # mxg_score
+
 SUCCESS, ERROR_INVALID_VALUE, ERROR_NOT_SUPPORTED, ERROR_LAUNCH = 0, 1, 2, 3
 MAX_GROUPS = 1024
 MAX_K = 1 << 22  # largest K of the grouped GEMMs (MXG_MAX_K)
@@ -36,7 +48,10 @@ EXPORTED = ("mx_grouped_quantize", "mx_grouped_quantize_gather", "mx_grouped_qua
             "mx_grouped_matmul_swiglu_nvfp4", "mx_silu_quantize_nvfp4", "mx_grouped_quantize_padded",
             "mx_grouped_matmul_padded", "mx_grouped_matmul_swiglu_padded",
             "mx_grouped_quantize_nvfp4_padded", "mx_grouped_matmul_nvfp4_padded", "mx_prepared_weights_bytes",
-            "mx_prepare_weights_fp8", "mx_grouped_matmul_prepared", "mxg_clock_probe", "mxg_fp8_tile",
+            "mx_prepare_weights_fp8", "mx_grouped_matmul_prepared", "mx_moe_topk", "mx_moe_topk_backward",
+            "mx_moe_sort", "mx_moe_permute", "mx_moe_permute_backward", "mx_moe_combine_backward",
+            "mx_grouped_quantize_block128", "mx_grouped_quantize_block128_scatter", "mx_quantize_weights_block128",
+            "mx_grouped_matmul_block128", "mx_silu_quantize_block128", "mx_silu_backward_block128", "mxg_clock_probe", "mxg_fp8_tile",
             "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
 
 
@@ -97,6 +112,23 @@ def lib() -> ctypes.CDLL:
         L.mx_prepare_weights_fp8.restype = ctypes.c_int
         L.mx_grouped_matmul_prepared.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I64, _I64, _I64, _P]
         L.mx_grouped_matmul_prepared.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        for name, args in (
+                ("mx_moe_topk", [ctypes.c_int, ctypes.c_int, _P, _P, _I64, _I32, _I32, _I32, f32, _P, _P, _P]),
+                ("mx_moe_topk_backward", [ctypes.c_int, ctypes.c_int, _P, _P, _P, _I64, _I32, _I32, _I32, f32, _P, _P]),
+                ("mx_moe_sort", [_P, _I64, _I32, _I32, _P, _P, _P, _P]),
+                ("mx_moe_permute", [_P, _I64, _I64, _P, _I32, _P, _I64, _P]),
+                ("mx_moe_permute_backward", [_P, _I64, _I64, _P, _I64, _I32, _P, _P]),
+                ("mx_moe_combine_backward", [_P, _P, _I64, _I64, _P, _P, _I64, _I32, _P, _P, _P]),
+                ("mx_grouped_quantize_block128", [_P, _P, _P, _P, _I32, _I64, _I64, _P]),
+                ("mx_grouped_quantize_block128_scatter", [_P, _I64, _P, _I32, _P, _P, _P, _I32, _I64, _I64, _P]),
+                ("mx_quantize_weights_block128", [_P, _I32, _I64, _I64, _P, _P, _P, _P, _P]),
+                ("mx_grouped_matmul_block128", [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I64, _I64, _I64, _I64, _P]),
+                ("mx_silu_quantize_block128", [_P, _P, _P, _P, _I32, _I64, _I64, _P]),
+                ("mx_silu_backward_block128", [_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _P])):
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
         L.mxg_validation_message.argtypes = []
         L.mxg_validation_message.restype = ctypes.c_char_p
         L.mxg_routing_violation.argtypes = [_P, _P, _I32, _I32, _I64, ctypes.c_char_p, _I64]
@@ -709,3 +741,314 @@ def mx_grouped_matmul_nvfp4_padded(a_q, a_scales, a_scales_offsets, b_q, b_scale
                                                 _ptr(row_offsets), _ptr(expert_ids), G, E, T, N, K,
                                                 int(max_rows_per_group_hint), _stream(a_q)),
            "mx_grouped_matmul_nvfp4_padded")
+
+
+# ----------------------------------------------------------------------------- router, routing plan, block-128 FP8
+_LOGITS = (torch.float32, torch.bfloat16)
+
+
+def _run(name: str, dev, *args) -> None:
+    """Call the entry point `name` on dev's current stream (appended), with dev the current device."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != SUCCESS:
+        raise MxgError(status, name)
+
+
+def _groups(row_offsets, dev) -> int:
+    """num_groups of a 1-D row_offsets."""
+    _expect(row_offsets, "row_offsets", _U32, None, dev)
+    if row_offsets.dim() != 1 or row_offsets.numel() < 1:
+        raise ValueError("row_offsets must be [num_groups + 1]")
+    return row_offsets.numel() - 1
+
+
+def _matrix(t, name: str, dtypes, dev=None):
+    """The two sizes of a contiguous 2-D GPU tensor."""
+    _expect(t, name, dtypes, None, dev)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _blocks128(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _top_k(row_of_slot, num_tokens: int, dev) -> int:
+    """top_k of a flat row_of_slot of num_tokens tokens (1 where there are none)."""
+    _expect(row_of_slot, "row_of_slot", _I32T, None, dev)
+    n = row_of_slot.numel()
+    if num_tokens == 0:
+        if n:
+            raise ValueError("row_of_slot must hold num_tokens * top_k entries")
+        return 1
+    if n == 0 or n % num_tokens:
+        raise ValueError("row_of_slot must hold num_tokens * top_k entries")
+    return n // num_tokens
+
+
+def _apart(a, b, names: str) -> None:
+    """Refuse two tensors that share memory."""
+    if a.numel() and b.numel():
+        a0, b0 = a.data_ptr(), b.data_ptr()
+        if a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size():
+            raise ValueError(f"{names} may not overlap")
+
+
+def mx_moe_topk(score: int, logits, topk_ids, topk_weights, bias=None, renormalize: bool = True,
+                scale: float = 1.0) -> None:
+    """The router: each token's top_k experts of logits [S, E] (fp32 or bf16) by softmax or
+    sigmoid score, or by score + bias (fp32 [E]), into topk_ids int32 [S, k], with their
+    weights scale * score (renormalised over the token's experts or not) in topk_weights fp32 [S, k]."""
+    S, E = _matrix(logits, "logits", _LOGITS)
+    dev = logits.device
+    k = _matrix(topk_ids, "topk_ids", _I32T, dev)[1]
+    _expect(topk_ids, "topk_ids", _I32T, (S, k), dev)
+    _expect(topk_weights, "topk_weights", _F32, (S, k), dev)
+    if bias is not None:
+        _expect(bias, "bias", _F32, (E,), dev)
+    _run("mx_moe_topk", dev, F32 if logits.dtype == torch.float32 else BF16, score, logits.data_ptr(),
+         None if bias is None else bias.data_ptr(), S, E, k, 1 if renormalize else 0, scale, topk_ids.data_ptr(),
+         topk_weights.data_ptr())
+
+
+def mx_moe_topk_backward(score: int, logits, topk_ids, dweights, dlogits, renormalize: bool = True,
+                         scale: float = 1.0) -> None:
+    """The gradient of mx_moe_topk's weights with respect to the logits, for the experts
+    topk_ids that were chosen: dweights fp32 [S, k] -> dlogits [S, E] of the logits' type."""
+    S, E = _matrix(logits, "logits", _LOGITS)
+    dev = logits.device
+    k = _matrix(topk_ids, "topk_ids", _I32T, dev)[1]
+    _expect(topk_ids, "topk_ids", _I32T, (S, k), dev)
+    _expect(dweights, "dweights", _F32, (S, k), dev)
+    _expect(dlogits, "dlogits", (logits.dtype,), (S, E), dev)
+    _run("mx_moe_topk_backward", dev, F32 if logits.dtype == torch.float32 else BF16, score, logits.data_ptr(),
+         topk_ids.data_ptr(), dweights.data_ptr(), S, E, k, 1 if renormalize else 0, scale, dlogits.data_ptr())
+
+
+def mx_moe_sort(topk_ids, row_offsets, row_of_slot, slot_of_row) -> None:
+    """The routing plan of topk_ids int32 [S, k]: row_offsets [E + 1] (E from its size),
+    row_of_slot and slot_of_row int32 [S * k]; ids outside [0, E) are dropped slots."""
+    S, k = _matrix(topk_ids, "topk_ids", _I32T)
+    dev = topk_ids.device
+    E = _groups(row_offsets, dev)
+    _expect(row_of_slot, "row_of_slot", _I32T, (S * k,), dev)
+    _expect(slot_of_row, "slot_of_row", _I32T, (S * k,), dev)
+    _run("mx_moe_sort", dev, topk_ids.data_ptr(), S, k, E, row_offsets.data_ptr(), row_of_slot.data_ptr(),
+         slot_of_row.data_ptr())
+
+
+def mx_moe_permute(x, row_of_slot, rows) -> None:
+    """Token rows x [S, H] bf16 copied to the routed rows [T, H] of their slots
+    (row_of_slot int32 [S * top_k]); rows no slot names are left untouched."""
+    S, H = _matrix(x, "x", _BF16)
+    dev = x.device
+    T = _matrix(rows, "rows", _BF16, dev)[0]
+    _expect(rows, "rows", _BF16, (T, H), dev)
+    k = _top_k(row_of_slot, S, dev)
+    _apart(x, rows, "x and rows")
+    _run("mx_moe_permute", dev, x.data_ptr(), S, H, row_of_slot.data_ptr(), k, rows.data_ptr(), T)
+
+
+def mx_moe_permute_backward(drows, row_of_slot, dx) -> None:
+    """The gradient of mx_moe_permute: dx [S, H] bf16 = the sum of each token's slots' rows of drows [T, H] bf16."""
+    T, H = _matrix(drows, "drows", _BF16)
+    dev = drows.device
+    S = _matrix(dx, "dx", _BF16, dev)[0]
+    _expect(dx, "dx", _BF16, (S, H), dev)
+    k = _top_k(row_of_slot, S, dev)
+    _apart(drows, dx, "drows and dx")
+    _run("mx_moe_permute_backward", dev, drows.data_ptr(), T, H, row_of_slot.data_ptr(), S, k, dx.data_ptr())
+
+
+def mx_moe_combine_backward(dout, y, row_of_slot, weights, dy, dweights) -> None:
+    """The gradient of mx_moe_combine: from dout [S, H] bf16, the routed rows y [T, H] bf16 and
+    the weights fp32 [S * top_k], dy [T, H] bf16 (rows no slot names left untouched) and
+    dweights fp32 [S * top_k]."""
+    S, H = _matrix(dout, "dout", _BF16)
+    dev = dout.device
+    T = _matrix(y, "y", _BF16, dev)[0]
+    _expect(y, "y", _BF16, (T, H), dev)
+    _expect(dy, "dy", _BF16, (T, H), dev)
+    k = _top_k(row_of_slot, S, dev)
+    n = row_of_slot.numel()
+    _expect(weights, "weights", _F32, None, dev)
+    _expect(dweights, "dweights", _F32, None, dev)
+    if weights.numel() != n or dweights.numel() != n:
+        raise ValueError("weights and dweights must hold num_tokens * top_k entries")
+    _apart(dy, y, "dy and y")
+    _apart(dy, dout, "dy and dout")
+    _run("mx_moe_combine_backward", dev, dout.data_ptr(), y.data_ptr(), T, H, row_of_slot.data_ptr(),
+         weights.data_ptr(), S, k, dy.data_ptr(), dweights.data_ptr())
+
+
+def mx_grouped_quantize_block128(x, q, scales, row_offsets) -> None:
+    """Grouped quantize of bf16 x [T, K] to e4m3 q u8 [T, K] with an fp32 scale per 1 x 128
+    block in scales [T, ceil(K/128)]; only covered rows are written."""
+    T, K = _matrix(x, "x", _BF16)
+    dev = x.device
+    _expect(q, "q", _U8, (T, K), dev)
+    _expect(scales, "scales", _F32, (T, _blocks128(K)), dev)
+    G = _groups(row_offsets, dev)
+    _run("mx_grouped_quantize_block128", dev, x.data_ptr(), q.data_ptr(), scales.data_ptr(), row_offsets.data_ptr(),
+         G, T, K)
+
+
+def mx_grouped_quantize_block128_scatter(x_tokens, row_of_slot, q, scales, row_offsets) -> None:
+    """Token-major form: each token row of x_tokens [S, K] bf16 is quantized once into its
+    routed rows row_of_slot[s*top_k + k] of q [T, K] and scales [T, ceil(K/128)]."""
+    S, K = _matrix(x_tokens, "x_tokens", _BF16)
+    dev = x_tokens.device
+    T = _matrix(q, "q", _U8, dev)[0]
+    _expect(q, "q", _U8, (T, K), dev)
+    _expect(scales, "scales", _F32, (T, _blocks128(K)), dev)
+    k = _top_k(row_of_slot, S, dev)
+    G = _groups(row_offsets, dev)
+    _run("mx_grouped_quantize_block128_scatter", dev, x_tokens.data_ptr(), S, row_of_slot.data_ptr(), k, q.data_ptr(),
+         scales.data_ptr(), row_offsets.data_ptr(), G, T, K)
+
+
+def mx_quantize_weights_block128(w, q, scales, q_t=None, scales_t=None) -> None:
+    """Weights w [E, N, K] bf16 to e4m3 q u8 [E, N, K] with an fp32 scale per 128 x 128 block
+    in scales [E, ceil(N/128), ceil(K/128)]; with q_t and scales_t also the transposed
+    weights [E, K, N] and [E, ceil(K/128), ceil(N/128)] (the same codes)."""
+    _expect(w, "w", _BF16)
+    if w.dim() != 3:
+        raise ValueError("w must be [num_experts, N, K]")
+    E, N, K = w.shape
+    dev = w.device
+    _expect(q, "q", _U8, (E, N, K), dev)
+    _expect(scales, "scales", _F32, (E, _blocks128(N), _blocks128(K)), dev)
+    if (q_t is None) != (scales_t is None):
+        raise ValueError("q_t and scales_t are given together or not at all")
+    if q_t is not None:
+        _expect(q_t, "q_t", _U8, (E, K, N), dev)
+        _expect(scales_t, "scales_t", _F32, (E, _blocks128(K), _blocks128(N)), dev)
+    _run("mx_quantize_weights_block128", dev, w.data_ptr(), E, N, K, q.data_ptr(), scales.data_ptr(),
+         None if q_t is None else q_t.data_ptr(), None if scales_t is None else scales_t.data_ptr())
+
+
+def mx_grouped_matmul_block128(a_q, a_scales, b_q, b_scales, c, row_offsets, expert_ids,
+                               max_rows_per_group_hint: int = 0) -> None:
+    """Ragged grouped GEMM of block-scaled e4m3 into bf16 c [T, N]: a_q [T, K], a_scales fp32
+    [T, ceil(K/128)], b_q [E, N, K], b_scales fp32 [E, ceil(N/128), ceil(K/128)]."""
+    T, K = _matrix(a_q, "a_q", _U8)
+    dev = a_q.device
+    _expect(b_q, "b_q", _U8, None, dev)
+    if b_q.dim() != 3:
+        raise ValueError("b_q must be [num_experts, N, K]")
+    E, N = b_q.shape[0], b_q.shape[1]
+    _expect(b_q, "b_q", _U8, (E, N, K), dev)
+    _expect(a_scales, "a_scales", _F32, (T, _blocks128(K)), dev)
+    _expect(b_scales, "b_scales", _F32, (E, _blocks128(N), _blocks128(K)), dev)
+    _expect(c, "c", _BF16, (T, N), dev)
+    G = _groups(row_offsets, dev)
+    _expect(expert_ids, "expert_ids", _I32T, (G,), dev)
+    _run("mx_grouped_matmul_block128", dev, a_q.data_ptr(), a_scales.data_ptr(), b_q.data_ptr(), b_scales.data_ptr(),
+         c.data_ptr(), row_offsets.data_ptr(), expert_ids.data_ptr(), G, E, T, N, K, int(max_rows_per_group_hint))
+
+
+def mx_silu_quantize_block128(h, y_q, y_scales, row_offsets) -> None:
+    """SwiGLU of bf16 h [T, 2I] (gate/up interleaved by column), requantized from fp32 to e4m3
+    y_q u8 [T, I] with an fp32 scale per 1 x 128 block in y_scales [T, ceil(I/128)]."""
+    T, N2 = _matrix(h, "h", _BF16)
+    if N2 % 2:
+        raise ValueError("h must be [total_rows, 2I]")
+    I = N2 // 2
+    dev = h.device
+    _expect(y_q, "y_q", _U8, (T, I), dev)
+    _expect(y_scales, "y_scales", _F32, (T, _blocks128(I)), dev)
+    G = _groups(row_offsets, dev)
+    _run("mx_silu_quantize_block128", dev, h.data_ptr(), y_q.data_ptr(), y_scales.data_ptr(), row_offsets.data_ptr(),
+         G, T, I)
+
+
+def mx_silu_backward_block128(h, dy, row_offsets, dh=None, dh_q=None, dh_scales=None) -> None:
+    """The gradient of SwiGLU: dy [T, I] bf16 and h [T, 2I] bf16 -> dh [T, 2I] bf16 (may be h
+    itself) and / or its requant dh_q u8 [T, 2I], dh_scales fp32 [T, ceil(2I/128)]."""
+    T, N2 = _matrix(h, "h", _BF16)
+    if N2 % 2:
+        raise ValueError("h must be [total_rows, 2I]")
+    I = N2 // 2
+    dev = h.device
+    _expect(dy, "dy", _BF16, (T, I), dev)
+    if (dh_q is None) != (dh_scales is None) or (dh is None and dh_q is None):
+        raise ValueError("give dh, or dh_q with dh_scales, or all three")
+    if dh is not None:
+        _expect(dh, "dh", _BF16, (T, N2), dev)
+        _apart(dh, dy, "dh and dy")
+        if dh.data_ptr() != h.data_ptr():
+            _apart(dh, h, "dh (unless it is h) and h")
+    if dh_q is not None:
+        _expect(dh_q, "dh_q", _U8, (T, N2), dev)
+        _expect(dh_scales, "dh_scales", _F32, (T, _blocks128(N2)), dev)
+    G = _groups(row_offsets, dev)
+    _run("mx_silu_backward_block128", dev, h.data_ptr(), dy.data_ptr(), None if dh is None else dh.data_ptr(),
+         None if dh_q is None else dh_q.data_ptr(), None if dh_scales is None else dh_scales.data_ptr(),
+         row_offsets.data_ptr(), G, T, I)
+
+
+# ----------------------------------------------------------------------------- allocating forms
+def moe_topk(score: int, logits, top_k: int, bias=None, renormalize: bool = True, scale: float = 1.0):
+    """Returns (topk_ids int32 [S, top_k], topk_weights fp32 [S, top_k])."""
+    ids = torch.empty((logits.shape[0], top_k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((logits.shape[0], top_k), dtype=torch.float32, device=logits.device)
+    mx_moe_topk(score, logits, ids, weights, bias, renormalize, scale)
+    return ids, weights
+
+
+def moe_sort(topk_ids, num_experts: int):
+    """Returns (row_offsets [num_experts + 1], row_of_slot, slot_of_row), int32."""
+    off = torch.empty((num_experts + 1,), dtype=torch.int32, device=topk_ids.device)
+    ros = torch.empty((topk_ids.numel(),), dtype=torch.int32, device=topk_ids.device)
+    sor = torch.empty((topk_ids.numel(),), dtype=torch.int32, device=topk_ids.device)
+    mx_moe_sort(topk_ids, off, ros, sor)
+    return off, ros, sor
+
+
+def moe_permute(x, row_of_slot, total_rows: int):
+    """Returns the routed rows [total_rows, H]; rows no slot names are zero."""
+    rows = torch.zeros((total_rows, x.shape[1]), dtype=torch.bfloat16, device=x.device)
+    mx_moe_permute(x, row_of_slot, rows)
+    return rows
+
+
+def quantize_block128(x, row_offsets):
+    """Returns (q, scales); rows no group covers are zero."""
+    T, K = x.shape
+    q = torch.zeros((T, K), dtype=torch.uint8, device=x.device)
+    s = torch.zeros((T, _blocks128(K)), dtype=torch.float32, device=x.device)
+    mx_grouped_quantize_block128(x, q, s, row_offsets)
+    return q, s
+
+
+def quantize_weights_block128(w, transposed: bool = False):
+    """Returns (q, scales) of bf16 weights [E, N, K], or (q, scales, q_t, scales_t)."""
+    E, N, K = w.shape
+    q = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
+    s = torch.empty((E, _blocks128(N), _blocks128(K)), dtype=torch.float32, device=w.device)
+    if not transposed:
+        mx_quantize_weights_block128(w, q, s)
+        return q, s
+    qt = torch.empty((E, K, N), dtype=torch.uint8, device=w.device)
+    st = torch.empty((E, _blocks128(K), _blocks128(N)), dtype=torch.float32, device=w.device)
+    mx_quantize_weights_block128(w, q, s, qt, st)
+    return q, s, qt, st
+
+
+def grouped_matmul_block128(a_q, a_scales, b_q, b_scales, row_offsets, expert_ids, max_rows_per_group_hint=0):
+    c = torch.zeros((a_q.shape[0], b_q.shape[1]), dtype=torch.bfloat16, device=a_q.device)
+    mx_grouped_matmul_block128(a_q, a_scales, b_q, b_scales, c, row_offsets, expert_ids, max_rows_per_group_hint)
+    return c
+
+
+def silu_quantize_block128(h, row_offsets):
+    T, I = h.shape[0], h.shape[1] // 2
+    yq = torch.zeros((T, I), dtype=torch.uint8, device=h.device)
+    ys = torch.zeros((T, _blocks128(I)), dtype=torch.float32, device=h.device)
+    mx_silu_quantize_block128(h, yq, ys, row_offsets)
+    return yq, ys

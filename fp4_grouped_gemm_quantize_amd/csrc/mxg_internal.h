@@ -84,6 +84,36 @@ int fp8_tile_choice(const GemmProblem& p);
 int64_t prepared_weights_bytes(int64_t E, int64_t N, int64_t K);
 hipError_t launch_prepare_weights(const void* b, int64_t E, int64_t N, int64_t K, void* out, hipStream_t stream);
 
+// The router and the routing plan (route.hip).  type: 0 fp32, 1 bf16 logits; score: 0 softmax, 1 sigmoid.
+hipError_t launch_topk(int type, int score, const void* logits, const float* bias, int64_t ntok, int E, int top_k,
+                       bool renorm, float scale, int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_topk_backward(int type, int score, const void* logits, const int32_t* ids, const float* dweights,
+                                int64_t ntok, int E, int top_k, bool renorm, float scale, void* dlogits,
+                                hipStream_t stream);
+hipError_t launch_sort(const int32_t* ids, int64_t nslots, int E, uint32_t* off, int32_t* row_of_slot,
+                       int32_t* slot_of_row, hipStream_t stream);
+
+// Rows into expert order and the gradients of the way there and back (combine.hip).
+hipError_t launch_permute(const void* x, int64_t ntok, int64_t H, const int32_t* row_of_slot, int top_k, void* rows,
+                          int64_t T, hipStream_t stream);
+hipError_t launch_permute_backward(const void* drows, int64_t T, int64_t H, const int32_t* row_of_slot, int64_t ntok,
+                                   int top_k, void* dx, hipStream_t stream);
+hipError_t launch_combine_backward(const void* dout, const void* y, int64_t T, int64_t H, const int32_t* row_of_slot,
+                                   const float* weights, int64_t ntok, int top_k, void* dy, float* dweights,
+                                   hipStream_t stream);
+
+// FP8 with 128-element block scales (block128.hip, gemm_block128.hip).  row_of_slot == nullptr: row-major, x has T rows.
+hipError_t launch_quantize_block128(const void* x, int64_t ntok, const int32_t* row_of_slot, int top_k, void* q,
+                                    float* scales, const uint32_t* off, int G, int64_t T, int64_t K,
+                                    hipStream_t stream);
+hipError_t launch_quantize_weights_block128(const void* w, int64_t E, int64_t N, int64_t K, void* q, float* scales,
+                                            void* q_t, float* scales_t, hipStream_t stream);
+hipError_t launch_silu_quantize_block128(const void* h, void* yq, float* ys, const uint32_t* off, int G, int64_t T,
+                                         int64_t I, hipStream_t stream);
+hipError_t launch_silu_backward_block128(const void* h, const void* dy, void* dh, void* dh_q, float* dh_scales,
+                                         const uint32_t* off, int G, int64_t T, int64_t I, hipStream_t stream);
+hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream);
+
 // One wave: out[0] = shader-clock ticks, out[1] = 100 MHz ticks (>= ticks) of one sleep window.
 hipError_t launch_clock_probe(unsigned long long* out, unsigned long long ticks, hipStream_t stream);
 

@@ -1,0 +1,451 @@
+// route.hip -- the router (top-k expert choice and its gradient) and the routing
+// plan (a stable counting sort of the slots by expert), for gfx950.
+//
+// (Struct_ep_dispatch_mxfp4: topk_ids, row_offsets and src_info; the pages name
+//  these arrays and do not say how they are made.)
+//
+// All three are small integer or scalar jobs over [tokens, experts] or [slots]
+// arrays, bound by latency: each is one launch, without workspace or atomics,
+// so results do not depend on timing.
+#include <type_traits>
+
+#include "mxg_device.h"
+#include "mxg_internal.h"
+
+namespace mxg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------------
+// Cross-lane exchange inside a token's LPT lanes.  Within 16 lanes (a DPP row)
+// the four steps are register moves: lane ^ 1 and lane ^ 2 (quad permutes),
+// then the mirrors within 8 and 16 lanes, which pair values that are by then
+// equal inside each quad / half.  Wider groups add shuffles over 16 and 32.
+template <int STEP>
+__device__ __forceinline__ uint32_t exchange(uint32_t v) {
+    if constexpr (STEP == 0) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xf, 0xf, false);
+    else if constexpr (STEP == 1) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xf, 0xf, false);
+    else if constexpr (STEP == 2) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xf, 0xf, false);
+    else if constexpr (STEP == 3) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xf, 0xf, false);
+    else return (uint32_t)__shfl_xor((int)v, 1 << STEP, kWave);
+}
+template <int STEP>
+__device__ __forceinline__ uint64_t exchange(uint64_t v) {
+    return ((uint64_t)exchange<STEP>((uint32_t)(v >> 32)) << 32) | exchange<STEP>((uint32_t)v);
+}
+template <int STEP>
+__device__ __forceinline__ float exchange(float v) {
+    return __uint_as_float(exchange<STEP>(__float_as_uint(v)));
+}
+template <int STEP>
+__device__ __forceinline__ double exchange(double v) {
+    return __longlong_as_double((long long)exchange<STEP>((uint64_t)__double_as_longlong(v)));
+}
+
+// v combined over a token's LPT lanes by f (the result in every lane).
+template <int LPT, class T, class F>
+__device__ __forceinline__ T reduce(T v, F f) {
+    v = f(v, exchange<0>(v));
+    v = f(v, exchange<1>(v));
+    v = f(v, exchange<2>(v));
+    v = f(v, exchange<3>(v));
+    if constexpr (LPT == 64) {
+        v = f(v, exchange<4>(v));
+        v = f(v, exchange<5>(v));
+    }
+    return v;
+}
+template <int LPT, class T>
+__device__ __forceinline__ T sum_over(T v) {
+    return reduce<LPT>(v, [](T a, T b) { return a + b; });
+}
+template <int LPT>
+__device__ __forceinline__ float max_over(float v) {
+    return reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16(v); }
+
+// Keys in an order that unsigned comparison keeps, 0 for a value that may not
+// be chosen (-infinity, NaN): every other value maps above 0.  Adding zero
+// turns -0 into +0, which compare equal.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return v > -INFINITY ? ((u >> 31) ? ~u : u | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return v > -(double)INFINITY ? ((u >> 63) ? ~u : u | 0x8000000000000000ull) : 0ull;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// log(1 / (1 + e^-x)), exact where the sigmoid itself underflows
+__device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.0f) - log1pf(expf(-fabsf(x))); }
+
+// ---------------------------------------------------------------------------
+// LPT lanes hold a token's logits, expert i in lane i % LPT (element i / LPT),
+// so loads are coalesced and a lane's elements rise with their index.  Each of
+// the top_k rounds takes the largest key of the lane's own elements, then of
+// the token's lanes (equal keys: the lower index), and clears the winner's.
+// 16 lanes a token hold four tokens a wave: a round is then VPL compares and
+// four register exchanges for all four.  Lane j ends with slot j, so 16 lanes
+// serve top_k <= 16.
+template <class LT, int LPT, int VPL, bool BIASED>
+__global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ logits, const float* __restrict__ bias,
+                                                        int64_t ntok, int E, int top_k, int score, bool renorm,
+                                                        float scale, int32_t* __restrict__ ids,
+                                                        float* __restrict__ weights) {
+    const int sub = threadIdx.x % LPT;
+    for (int64_t t0 = (int64_t)blockIdx.x * (kThreads / LPT); t0 < ntok; t0 += (int64_t)gridDim.x * (kThreads / LPT)) {
+        const int64_t t = t0 + threadIdx.x / LPT;
+        using Key = typename std::conditional<BIASED, uint64_t, uint32_t>::type;
+        const bool on = t < ntok;  // the lanes of a token past the end stay for the exchanges
+        const LT* row = logits + (on ? t : 0) * E;
+
+        float x[VPL];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int i = v * LPT + sub;
+            x[v] = on && i < E ? load_logit(row + i) : -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) top = fmaxf(top, x[v]);
+        top = max_over<LPT>(top);
+
+        Key key[VPL];
+        if constexpr (BIASED) {
+            double total = 1.0;
+            if (score == 0) {
+                double z = 0.0;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    if (v * LPT + sub < E) z += exp((double)x[v] - (double)top);
+                total = sum_over<LPT>(z);
+            }
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const int i = v * LPT + sub;
+                key[v] = 0;
+                if (i < E && x[v] > -INFINITY) {
+                    const double s = score == 0 ? exp((double)x[v] - (double)top) / total
+                                                : 1.0 / (1.0 + exp(-(double)x[v]));
+                    key[v] = order_key(s + (double)bias[i]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) key[v] = order_key(x[v]);
+        }
+
+        int32_t my_id = -1;
+        for (int k = 0; k < top_k; ++k) {
+            Key best = key[0];
+            uint32_t at = (uint32_t)sub;
+#pragma unroll
+            for (int v = 1; v < VPL; ++v)
+                if (key[v] > best) {
+                    best = key[v];
+                    at = (uint32_t)(v * LPT + sub);
+                }
+            auto step = [&](Key ok, uint32_t oi) {
+                const bool take = ok > best || (ok == best && oi < at);
+                best = take ? ok : best;
+                at = take ? oi : at;
+            };
+            step(exchange<0>(best), exchange<0>(at));
+            step(exchange<1>(best), exchange<1>(at));
+            step(exchange<2>(best), exchange<2>(at));
+            step(exchange<3>(best), exchange<3>(at));
+            if constexpr (LPT == 64) {
+                step(exchange<4>(best), exchange<4>(at));
+                step(exchange<5>(best), exchange<5>(at));
+            }
+            if (sub == k) my_id = best ? (int32_t)at : -1;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if ((uint32_t)(v * LPT + sub) == at) key[v] = 0;
+        }
+
+        const bool live = my_id >= 0;
+        const float mine = live ? load_logit(row + my_id) : 0.0f;
+        float w;
+        if (renorm) {
+            const float l = !live ? -INFINITY : score == 0 ? mine : log_sigmoid(mine);
+            const float m = max_over<LPT>(l);
+            w = live ? expf(l - m) : 0.0f;
+            w = w / sum_over<LPT>(w);
+        } else if (score == 0) {
+            float z = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if (v * LPT + sub < E) z += expf(x[v] - top);
+            w = expf(mine - top) / sum_over<LPT>(z);
+        } else {
+            w = sigmoid(mine);
+        }
+        if (on && sub < top_k) {
+            ids[t * top_k + sub] = my_id;
+            weights[t * top_k + sub] = live ? scale * w : 0.0f;
+        }
+    }
+}
+
+// The gradient: lane j forms slot j's g_j (the gradient of the log of its
+// score, and for the sigmoid of its logit), then every lane adds the slots that
+// name one of its own experts.  The logits are read whole only where the
+// gradient needs them (softmax without renormalisation).
+template <class LT, int LPT, int VPL>
+__global__ __launch_bounds__(kThreads) void topk_backward_kernel(const LT* __restrict__ logits,
+                                                                 const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ dweights, int64_t ntok,
+                                                                 int E, int top_k, int score, bool renorm, float scale,
+                                                                 LT* __restrict__ dlogits) {
+    const int sub = threadIdx.x % LPT;
+    for (int64_t t0 = (int64_t)blockIdx.x * (kThreads / LPT); t0 < ntok; t0 += (int64_t)gridDim.x * (kThreads / LPT)) {
+        const int64_t t = t0 + threadIdx.x / LPT;
+        const bool on = t < ntok;
+        const LT* row = logits + (on ? t : 0) * E;
+        int32_t id = -1;
+        float d = 0.0f, mine = -INFINITY;
+        if (on && sub < top_k) {
+            id = ids[t * top_k + sub];
+            if (id < 0 || id >= E) id = -1;
+            if (id >= 0) {
+                mine = load_logit(row + id);
+                d = scale * dweights[t * top_k + sub];
+            }
+        }
+        if (mine == -INFINITY) id = -1;  // its weight is 0 whatever the logit's neighbourhood
+        const bool live = id >= 0;
+
+        float g = 0.0f, top = 0.0f, total = 1.0f, x[VPL];
+        const bool whole = score == 0 && !renorm;
+        if (whole) {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const int i = v * LPT + sub;
+                x[v] = on && i < E ? load_logit(row + i) : -INFINITY;
+            }
+            top = x[0];
+#pragma unroll
+            for (int v = 1; v < VPL; ++v) top = fmaxf(top, x[v]);
+            top = max_over<LPT>(top);
+            float z = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if (v * LPT + sub < E) z += expf(x[v] - top);
+            total = sum_over<LPT>(z);
+            g = live ? expf(mine - top) / total * d : 0.0f;
+        } else if (renorm) {
+            const float l = !live ? -INFINITY : score == 0 ? mine : log_sigmoid(mine);
+            const float m = max_over<LPT>(l);
+            float r = live ? expf(l - m) : 0.0f;
+            r = r / sum_over<LPT>(r);
+            const float inner = sum_over<LPT>(live ? r * d : 0.0f);
+            g = live ? r * (d - inner) : 0.0f;
+        } else {
+            g = live ? sigmoid(mine) * d : 0.0f;
+        }
+        if (score == 1 && live) g *= sigmoid(-mine);
+        const float all = whole ? sum_over<LPT>(g) : 0.0f;
+
+        float acc[VPL];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) acc[v] = 0.0f;
+        const int first = (threadIdx.x & (kWave - 1)) - sub;  // the token's first lane in the wave
+        for (int k = 0; k < top_k; ++k) {
+            const int32_t ik = __shfl(id, first + k, kWave);
+            const float gk = __shfl(g, first + k, kWave);
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) acc[v] += ik == v * LPT + sub ? gk : 0.0f;
+        }
+        if (!on) continue;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int i = v * LPT + sub;
+            if (i >= E) continue;
+            float out = acc[v];
+            if (whole && all != 0.0f) out -= expf(x[v] - top) / total * all;
+            store_logit(dlogits + t * E + i, out);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Stable counting sort of n slots by expert id, one workgroup per expert.
+// Workgroup e reads every id (the whole list is a few hundred KB at most and
+// stays in L2): the ids below e give its first row, the ids equal to e, in slot
+// order, its rows.  A wave owns a contiguous stretch of the slots, so the rank
+// of a slot is the matches of the waves before, of its wave's steps before and
+// of the lanes before.  Reading the list once per expert costs E n / (bytes per
+// clock of an L1) and needs neither a workspace nor a second launch, nor
+// atomics whose speed falls when one expert takes most slots.  The steps'
+// matches are kept as one bit each; past 64 steps a wave (n > 65536) the second
+// pass reads the ids again.
+template <int NT>
+__global__ __launch_bounds__(NT) void sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                  uint32_t* __restrict__ off, int32_t* __restrict__ row_of_slot,
+                                                  int32_t* __restrict__ slot_of_row) {
+    constexpr int NW = NT / kWave;
+    __shared__ uint32_t s_less[NW], s_same[NW], s_valid[NW];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t e = blockIdx.x;
+    const int64_t steps = (n + (int64_t)NW * kWave - 1) / ((int64_t)NW * kWave);  // of 64 slots, per wave
+    const int64_t base = wave * steps * kWave;
+
+    uint32_t less = 0, same = 0, valid = 0;
+    uint64_t hits = 0;
+#pragma unroll 8
+    for (int64_t s = 0; s < steps; ++s) {
+        const int64_t i = base + s * kWave + lane;
+        const uint32_t id = i < n ? (uint32_t)ids[i] : 0xffffffffu;  // a negative id is a large one
+        less += id < e;
+        same += id == e;
+        valid += id < (uint32_t)E;
+        if (id == e && s < 64) hits |= 1ull << s;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        less += __shfl_xor(less, o, kWave);
+        same += __shfl_xor(same, o, kWave);
+        valid += __shfl_xor(valid, o, kWave);
+    }
+    if (lane == 0) {
+        s_less[wave] = less;
+        s_same[wave] = same;
+        s_valid[wave] = valid;
+    }
+    __syncthreads();
+    uint32_t first = 0, run = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        first += s_less[w];
+        run += w < wave ? s_same[w] : 0;
+        total += s_valid[w];
+    }
+    if (threadIdx.x == 0) {
+        off[e] = first;
+        if ((int)e == E - 1) off[E] = total;
+    }
+    run += first;
+    if (same) {  // wave-uniform
+        for (int64_t s = 0; s < steps; ++s) {
+            const int64_t i = base + s * kWave + lane;
+            bool hit;
+            if (steps <= 64) hit = (hits >> s) & 1;
+            else hit = i < n && (uint32_t)ids[i] == e;
+            const uint64_t m = __ballot(hit);
+            if (hit) {
+                const uint32_t r = run + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+                row_of_slot[i] = (int32_t)r;
+                slot_of_row[r] = (int32_t)i;
+            }
+            run += (uint32_t)__popcll(m);
+        }
+    }
+    // dropped slots and the rows past the last, shared out over the workgroups
+    if ((int64_t)total < n) {
+        for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < n; i += (int64_t)gridDim.x * NT) {
+            if ((uint32_t)ids[i] >= (uint32_t)E) row_of_slot[i] = -1;
+            if (i >= (int64_t)total) slot_of_row[i] = -1;
+        }
+    }
+}
+
+// A launch holds fewer than 2^32 threads; past this many workgroups they loop.
+unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20); }
+
+template <class LT, int LPT, int VPL>
+hipError_t topk_as(const void* logits, const float* bias, int64_t ntok, int E, int top_k, int score, bool renorm,
+                   float scale, int32_t* ids, float* weights, hipStream_t stream) {
+    constexpr int kTok = kThreads / LPT;
+    const dim3 grid(grid_of((ntok + kTok - 1) / kTok));
+    if (bias)
+        hipLaunchKernelGGL((topk_kernel<LT, LPT, VPL, true>), grid, dim3(kThreads), 0, stream,
+                           static_cast<const LT*>(logits), bias, ntok, E, top_k, score, renorm, scale, ids, weights);
+    else
+        hipLaunchKernelGGL((topk_kernel<LT, LPT, VPL, false>), grid, dim3(kThreads), 0, stream,
+                           static_cast<const LT*>(logits), bias, ntok, E, top_k, score, renorm, scale, ids, weights);
+    return hipGetLastError();
+}
+
+template <class LT, int LPT, int VPL>
+hipError_t topk_backward_as(const void* logits, const int32_t* ids, const float* dw, int64_t ntok, int E, int top_k,
+                            int score, bool renorm, float scale, void* dlogits, hipStream_t stream) {
+    constexpr int kTok = kThreads / LPT;
+    hipLaunchKernelGGL((topk_backward_kernel<LT, LPT, VPL>), dim3(grid_of((ntok + kTok - 1) / kTok)),
+                       dim3(kThreads), 0, stream, static_cast<const LT*>(logits), ids, dw, ntok, E, top_k, score,
+                       renorm, scale, static_cast<LT*>(dlogits));
+    return hipGetLastError();
+}
+
+// 16 lanes a token while they hold its experts in 16 elements and its slots in
+// one each; a whole wave otherwise.
+template <class LT, class F16x4, class F16x8, class F16x16, class F64x4, class F64x16>
+hipError_t choose(int E, int top_k, F16x4 a, F16x8 b, F16x16 c, F64x4 d, F64x16 e) {
+    if (top_k <= 16 && E <= 64) return a();
+    if (top_k <= 16 && E <= 128) return b();
+    if (top_k <= 16 && E <= 256) return c();
+    return E <= 256 ? d() : e();
+}
+
+template <class LT>
+hipError_t topk_type(int score, const void* lg, const float* bias, int64_t n, int E, int k, bool rn, float sc,
+                     int32_t* ids, float* w, hipStream_t s) {
+    return choose<LT>(
+        E, k, [&] { return topk_as<LT, 16, 4>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
+        [&] { return topk_as<LT, 16, 8>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
+        [&] { return topk_as<LT, 16, 16>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
+        [&] { return topk_as<LT, 64, 4>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
+        [&] { return topk_as<LT, 64, 16>(lg, bias, n, E, k, score, rn, sc, ids, w, s); });
+}
+
+template <class LT>
+hipError_t topk_backward_type(int score, const void* lg, const int32_t* ids, const float* dw, int64_t n, int E, int k,
+                              bool rn, float sc, void* dl, hipStream_t s) {
+    return choose<LT>(
+        E, k, [&] { return topk_backward_as<LT, 16, 4>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
+        [&] { return topk_backward_as<LT, 16, 8>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
+        [&] { return topk_backward_as<LT, 16, 16>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
+        [&] { return topk_backward_as<LT, 64, 4>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
+        [&] { return topk_backward_as<LT, 64, 16>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); });
+}
+
+}  // namespace
+
+hipError_t launch_topk(int type, int score, const void* logits, const float* bias, int64_t ntok, int E, int top_k,
+                       bool renorm, float scale, int32_t* ids, float* weights, hipStream_t stream) {
+    return type == 0 ? topk_type<float>(score, logits, bias, ntok, E, top_k, renorm, scale, ids, weights, stream)
+                     : topk_type<uint16_t>(score, logits, bias, ntok, E, top_k, renorm, scale, ids, weights, stream);
+}
+
+hipError_t launch_topk_backward(int type, int score, const void* logits, const int32_t* ids, const float* dweights,
+                                int64_t ntok, int E, int top_k, bool renorm, float scale, void* dlogits,
+                                hipStream_t stream) {
+    return type == 0 ? topk_backward_type<float>(score, logits, ids, dweights, ntok, E, top_k, renorm, scale, dlogits,
+                                                 stream)
+                     : topk_backward_type<uint16_t>(score, logits, ids, dweights, ntok, E, top_k, renorm, scale,
+                                                    dlogits, stream);
+}
+
+hipError_t launch_sort(const int32_t* ids, int64_t nslots, int E, uint32_t* off, int32_t* row_of_slot,
+                       int32_t* slot_of_row, hipStream_t stream) {
+    // four waves are enough for a serving step's slots and start sooner
+    if (nslots <= 4096)
+        hipLaunchKernelGGL(sort_kernel<256>, dim3((unsigned)E), dim3(256), 0, stream, ids, nslots, E, off, row_of_slot,
+                           slot_of_row);
+    else
+        hipLaunchKernelGGL(sort_kernel<1024>, dim3((unsigned)E), dim3(1024), 0, stream, ids, nslots, E, off,
+                           row_of_slot, slot_of_row);
+    return hipGetLastError();
+}
+
+}  // namespace mxg
