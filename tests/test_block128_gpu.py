@@ -209,18 +209,18 @@ def check_gemm(T, E, N, K, off, ids, seed=0, hint=0):
                                    offsets_gpu(np.asarray(off, np.uint32)), to_gpu(np.asarray(ids, np.int32)), hint)
     torch.cuda.synchronize()
     g.check()
-    got = g.view(torch.bfloat16).double().cpu()
-    val = torch.from_numpy(oracle.e4m3_value_array(np.arange(256, dtype=np.uint8)))
-    kb = torch.arange(K) // B
-    nb = torch.arange(N) // B
+    got = g.view(torch.bfloat16).double()
+    val = torch.from_numpy(oracle.e4m3_value_array(np.arange(256, dtype=np.uint8))).cuda()
+    kb = torch.arange(K, device="cuda") // B
+    nb = torch.arange(N, device="cuda") // B
     cov = np.zeros(T, bool)
     for g_i, e in enumerate(ids):
         lo, hi = min(int(off[g_i]), T), min(int(off[g_i + 1]), T)
         if hi <= lo or e < 0 or e >= E:
             continue
         cov[lo:hi] = True
-        av = val[torch.from_numpy(a[lo:hi].astype(np.int64))] * torch.from_numpy(sa[lo:hi]).double()[:, kb]
-        bv = val[torch.from_numpy(b[e].astype(np.int64))] * torch.from_numpy(sb[e]).double()[nb][:, kb]
+        av = val[to_gpu(a[lo:hi]).long()] * to_gpu(sa[lo:hi]).double()[:, kb]
+        bv = val[to_gpu(b[e]).long()] * to_gpu(sb[e]).double()[nb][:, kb]
         want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
         eights = av.abs().reshape(hi - lo, K // 8, 8).amax(2) @ bv.abs().reshape(N, K // 8, 8).amax(2).t()
         tol = (want.abs() * 2.0 ** -8 + 2.0 ** -134 + eights * 2.0 ** -9 + mag * (16 + nblk(K) + 3) * 2.0 ** -24)
@@ -255,6 +255,35 @@ def test_gemm_ragged():
     check_gemm(T, 6, 520, 640, [100, 100, 100], [5, 2])
     check_gemm(T, 3, 264, 256, [0, 100, 400, 100], [0, 1, 2])
     check_gemm(T, 3, 264, 256, [0, 100, 1 << 31], [0, 1])
+
+
+@pytest.mark.parametrize("T,E", [(4100, 3), (16500, 5)])
+@pytest.mark.parametrize("N,K", [(1000, 32), (1030, 288), (1001, 160), (776, 1152), (256, 2080)])
+def test_gemm_larger_tiles(T, E, N, K):
+    """Enough rows for the 128- and 256-row tiles (the sizes above run the row
+    kernel and the 32-row tiles): partial tiles, a group of one row, an empty one,
+    split last rounds, columns that fill no tile, one stage and many."""
+    cuts = sorted(np.random.default_rng(T + N).integers(0, T, E - 2).tolist())
+    off = [0, 1] + cuts + [cuts[-1] if cuts else 1, T]
+    ids = [i % E for i in range(len(off) - 1)]
+    check_gemm(T, E, N, K, off, ids, seed=N)
+
+
+def test_gemm_kernels_agree():
+    """One group's rows through every kernel the sizes around it select: each kernel
+    keeps a row's sum to itself, so more rows beside it change at most the last bit
+    (the row kernel joins its waves' sums in another order)."""
+    N, K, E = 520, 1184, 2
+    a, sa, b, sb = (to_gpu(v) for v in operands(16400, E, N, K, 21))
+    ids = to_gpu(np.array([1], np.int32))
+    ref = None
+    for T in (3, 40, 5000, 16400):
+        c = mxg.grouped_matmul_block128(a[:T].contiguous(), sa[:T].contiguous(), b, sb,
+                                        offsets_gpu(np.array([0, T], np.uint32)), ids)[:3].double()
+        if ref is None:
+            ref = c
+        # a neighbour in bf16 where the fp32 sums straddle a rounding border
+        assert bool(((c - ref).abs() <= ref.abs() * 2.0 ** -7 + 1e-3 * ref.abs().amax()).all())
 
 
 def test_gemm_many_groups():
