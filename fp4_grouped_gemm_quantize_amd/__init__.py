@@ -747,13 +747,22 @@ def mx_grouped_matmul_nvfp4_padded(a_q, a_scales, a_scales_offsets, b_q, b_scale
 _LOGITS = (torch.float32, torch.bfloat16)
 
 
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle without a Stream object around it, where torch has it: 0.1 us a call instead of 1.9.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _run(name: str, dev, *args) -> None:
     """Call the entry point `name` on dev's current stream (appended), with dev the current device."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn, index = getattr(lib(), name), dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status != SUCCESS:
         raise MxgError(status, name)
 
@@ -769,9 +778,10 @@ def _groups(row_offsets, dev) -> int:
 def _matrix(t, name: str, dtypes, dev=None):
     """The two sizes of a contiguous 2-D GPU tensor."""
     _expect(t, name, dtypes, None, dev)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    return shape
 
 
 def _blocks128(n: int) -> int:
@@ -806,8 +816,9 @@ def mx_moe_topk(score: int, logits, topk_ids, topk_weights, bias=None, renormali
     weights scale * score (renormalised over the token's experts or not) in topk_weights fp32 [S, k]."""
     S, E = _matrix(logits, "logits", _LOGITS)
     dev = logits.device
-    k = _matrix(topk_ids, "topk_ids", _I32T, dev)[1]
-    _expect(topk_ids, "topk_ids", _I32T, (S, k), dev)
+    rows, k = _matrix(topk_ids, "topk_ids", _I32T, dev)
+    if rows != S:
+        raise ValueError(f"topk_ids: {rows} rows, expected {S}")
     _expect(topk_weights, "topk_weights", _F32, (S, k), dev)
     if bias is not None:
         _expect(bias, "bias", _F32, (E,), dev)
@@ -822,8 +833,9 @@ def mx_moe_topk_backward(score: int, logits, topk_ids, dweights, dlogits, renorm
     topk_ids that were chosen: dweights fp32 [S, k] -> dlogits [S, E] of the logits' type."""
     S, E = _matrix(logits, "logits", _LOGITS)
     dev = logits.device
-    k = _matrix(topk_ids, "topk_ids", _I32T, dev)[1]
-    _expect(topk_ids, "topk_ids", _I32T, (S, k), dev)
+    rows, k = _matrix(topk_ids, "topk_ids", _I32T, dev)
+    if rows != S:
+        raise ValueError(f"topk_ids: {rows} rows, expected {S}")
     _expect(dweights, "dweights", _F32, (S, k), dev)
     _expect(dlogits, "dlogits", (logits.dtype,), (S, E), dev)
     _run("mx_moe_topk_backward", dev, F32 if logits.dtype == torch.float32 else BF16, score, logits.data_ptr(),

@@ -281,79 +281,150 @@ __global__ __launch_bounds__(kThreads) void topk_backward_kernel(const LT* __res
 // Stable counting sort of n slots by expert id, one workgroup per expert.
 // Workgroup e reads every id (the whole list is a few hundred KB at most and
 // stays in L2): the ids below e give its first row, the ids equal to e, in slot
-// order, its rows.  A wave owns a contiguous stretch of the slots, so the rank
-// of a slot is the matches of the waves before, of its wave's steps before and
-// of the lanes before.  Reading the list once per expert costs E n / (bytes per
-// clock of an L1) and needs neither a workspace nor a second launch, nor
-// atomics whose speed falls when one expert takes most slots.  The steps'
-// matches are kept as one bit each; past 64 steps a wave (n > 65536) the second
-// pass reads the ids again.
+// order, its rows.  A wave owns a contiguous stretch of the slots and takes 512
+// of them a step, eight a lane, so the rank of a slot is the matches of the waves
+// before, of its wave's steps before, of the lanes before (a scan of the lanes'
+// counts) and of its own lane's ids before.  Reading the list once per expert
+// needs neither a workspace nor a second launch, nor atomics whose speed falls
+// when one expert takes most slots.  Bound by instruction issue (a compare for
+// each of the two questions, the counts on the scalar unit).  Up to 8 steps a
+// wave (n <= 65536) the matches are kept as eight bits a step, past that the
+// second pass reads the ids again.  Measured, 65536 slots of 128 experts: 21 us
+// with one id a lane and step, 13 with four and a ballot for each.
+constexpr int kKeep = 8, kIds = 8;
+
+// Eight consecutive ids, -1 past the end.  inside (wave-uniform): all are before
+// it.  No branch either way, so a wave's loads leave together.
+typedef int ids4 __attribute__((ext_vector_type(4), aligned(4)));
+struct Ids {
+    int32_t v[kIds];
+};
+__device__ __forceinline__ Ids load_ids(const int32_t* __restrict__ ids, int64_t i, int64_t n, bool inside) {
+    Ids r;
+    if (inside) {
+        const ids4 lo = *reinterpret_cast<const ids4*>(ids + i), hi = *reinterpret_cast<const ids4*>(ids + i + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r.v[j] = lo[j];
+            r.v[j + 4] = hi[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kIds; ++j) {
+            const int32_t x = ids[i + j < n ? i + j : n - 1];
+            r.v[j] = i + j < n ? x : -1;
+        }
+    }
+    return r;
+}
+
+// The matches of eight ids with e, a bit each; counts the ids below e over the
+// wave (a negative id is a large one).
+__device__ __forceinline__ uint32_t match(const Ids& id, uint32_t e, uint32_t& less) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+        less += (uint32_t)__popcll(__ballot((uint32_t)id.v[j] < e));
+        m |= (uint32_t)id.v[j] == e ? 1u << j : 0u;
+    }
+    return m;
+}
+
+// Sum over the lanes up to and with this one: shifts inside rows of 16, then the
+// rows' last lanes broadcast on.
+__device__ __forceinline__ uint32_t lane_scan(uint32_t v) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false);  // row_shr:1
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1, 3
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2, 3
+    return v;
+}
+
 template <int NT>
 __global__ __launch_bounds__(NT) void sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
                                                   uint32_t* __restrict__ off, int32_t* __restrict__ row_of_slot,
                                                   int32_t* __restrict__ slot_of_row) {
     constexpr int NW = NT / kWave;
-    __shared__ uint32_t s_less[NW], s_same[NW], s_valid[NW];
+    __shared__ uint32_t s_less[NW], s_same[NW];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t e = blockIdx.x;
-    const int64_t steps = (n + (int64_t)NW * kWave - 1) / ((int64_t)NW * kWave);  // of 64 slots, per wave
-    const int64_t base = wave * steps * kWave;
+    constexpr int kStep = kIds * kWave;
+    const int64_t steps = (n + (int64_t)NW * kStep - 1) / ((int64_t)NW * kStep);  // per wave
+    const int64_t base = wave * steps * kStep + lane * kIds;  // this lane's first slot
+    const bool inside = (wave + 1) * steps * kStep <= n;
 
-    uint32_t less = 0, same = 0, valid = 0;
-    uint64_t hits = 0;
-#pragma unroll 8
-    for (int64_t s = 0; s < steps; ++s) {
-        const int64_t i = base + s * kWave + lane;
-        const uint32_t id = i < n ? (uint32_t)ids[i] : 0xffffffffu;  // a negative id is a large one
-        less += id < e;
-        same += id == e;
-        valid += id < (uint32_t)E;
-        if (id == e && s < 64) hits |= 1ull << s;
-    }
+    uint32_t less = 0, same = 0, hits[kKeep / 4] = {};  // hits: eight bits a step
+    if (steps <= kKeep) {
+        Ids v[kKeep];
+        if (inside) {
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        less += __shfl_xor(less, o, kWave);
-        same += __shfl_xor(same, o, kWave);
-        valid += __shfl_xor(valid, o, kWave);
+            for (int s = 0; s < kKeep; ++s)
+                if (s < steps) v[s] = load_ids(ids, base + (int64_t)s * kStep, n, true);
+        } else {
+#pragma unroll
+            for (int s = 0; s < kKeep; ++s)
+                if (s < steps) v[s] = load_ids(ids, base + (int64_t)s * kStep, n, false);
+        }
+#pragma unroll
+        for (int s = 0; s < kKeep; ++s)
+            if (s < steps) hits[s / 4] |= match(v[s], e, less) << (8 * (s % 4));
+#pragma unroll
+        for (int h = 0; h < kKeep / 4; ++h) same += __popc(hits[h]);
+    } else {
+#pragma unroll 4
+        for (int64_t s = 0; s < steps; ++s) same += __popc(match(load_ids(ids, base + s * kStep, n, inside), e, less));
     }
+    same = (uint32_t)__builtin_amdgcn_readlane((int)lane_scan(same), kWave - 1);
     if (lane == 0) {
         s_less[wave] = less;
         s_same[wave] = same;
-        s_valid[wave] = valid;
     }
     __syncthreads();
-    uint32_t first = 0, run = 0, total = 0;
+    uint32_t first = 0, run = 0, all_same = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         first += s_less[w];
         run += w < wave ? s_same[w] : 0;
-        total += s_valid[w];
+        all_same += s_same[w];
     }
+    const uint32_t total = first + all_same;  // of the last expert: the slots that were not dropped
     if (threadIdx.x == 0) {
         off[e] = first;
         if ((int)e == E - 1) off[E] = total;
     }
     run += first;
+    auto place = [&](int64_t i, uint32_t m) {  // the matches m of the step whose ids start at slot i
+        if (!__any(m != 0)) return;
+        const uint32_t mine = __popc(m), upto = lane_scan(mine);
+        uint32_t r = run + upto - mine;
+        while (m) {
+            const int32_t slot = (int32_t)i + (__ffs((int)m) - 1);
+            row_of_slot[slot] = (int32_t)r;
+            slot_of_row[r] = slot;
+            ++r;
+            m &= m - 1;
+        }
+        run += (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+    };
     if (same) {  // wave-uniform
-        for (int64_t s = 0; s < steps; ++s) {
-            const int64_t i = base + s * kWave + lane;
-            bool hit;
-            if (steps <= 64) hit = (hits >> s) & 1;
-            else hit = i < n && (uint32_t)ids[i] == e;
-            const uint64_t m = __ballot(hit);
-            if (hit) {
-                const uint32_t r = run + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-                row_of_slot[i] = (int32_t)r;
-                slot_of_row[r] = (int32_t)i;
+        if (steps <= kKeep) {
+#pragma unroll
+            for (int s = 0; s < kKeep; ++s)
+                if (s < steps) place(base + (int64_t)s * kStep, (hits[s / 4] >> (8 * (s % 4))) & 255u);
+        } else {
+            for (int64_t s = 0; s < steps; ++s) {
+                uint32_t unused = 0;
+                const int64_t i = base + s * kStep;
+                place(i, match(load_ids(ids, i, n, inside), e, unused));
             }
-            run += (uint32_t)__popcll(m);
         }
     }
-    // dropped slots and the rows past the last, shared out over the workgroups
-    if ((int64_t)total < n) {
-        for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < n; i += (int64_t)gridDim.x * NT) {
+    // the last expert's workgroup, which knows the total: dropped slots and the rows past the last
+    if ((int)e == E - 1 && (int64_t)total < n) {
+        for (int64_t i = threadIdx.x; i < n; i += NT) {
             if ((uint32_t)ids[i] >= (uint32_t)E) row_of_slot[i] = -1;
             if (i >= (int64_t)total) slot_of_row[i] = -1;
         }
