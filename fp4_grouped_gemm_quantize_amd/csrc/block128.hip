@@ -7,7 +7,12 @@
 //
 // All are HBM-bound streams read once and written once.  16 lanes x 8 elements
 // form a 1 x 128 block, so a wave's 16-byte loads stay contiguous and the block
-// maximum is four register exchanges.
+// maximum is four register exchanges.  Every wave takes one unit of work and
+// ends: where half the bytes are writes, persistent waves that load the next
+// unit while they encode the current one were slower at every grid size (SwiGLU
+// gradient of 32768 x 2048: 179 us with 8 resident workgroups a CU, 156 with 4,
+// 161 with 64, 146 so, 5.5 TB/s; scattered quantize of 8192 x 4096 to 65536
+// rows: 66, 66, 59, 59 us).
 #include "mxg_device.h"
 #include "mxg_internal.h"
 
@@ -42,25 +47,38 @@ __device__ __forceinline__ float amax_of16(float v) {
     return __uint_as_float(dpp_umax<0x140>(__float_as_uint(amax_of8(v))));
 }
 
-// Codes of 8 values under their block's scale: e4m3(x / scale), as IEEE binary32
-// division rounds it, by one fp64 product with the scale's fp64 reciprocal and
-// the rounding to binary32 (equal to the division for bf16 x and scale = amax /
-// 448, |x| <= amax; for other fp32 x the two can differ in the last bit).  The
-// clamp matters only where the scale is a subnormal that rounded down.
+// Codes of 8 values under their block's scale: e4m3(x / scale), the quotient as
+// IEEE binary32 division rounds it.  One division gives the scale's reciprocal r;
+// each quotient is then x r corrected by its exact remainder, q + (x - q scale) r
+// (Markstein), three operations instead of a division's ten.  Scales below 2^-60
+// are lifted by 2^64 with their values, an exact step, so that neither the
+// reciprocal overflows nor the remainder underflows.  The clamp matters only
+// where the scale is a subnormal that rounded down.
 __device__ __forceinline__ uint2 encode8(const float* x, float scale) {
     float f[8];
     if (scale == 0.0f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = x[i] * 0.0f;
     } else {
-        const double inv = 1.0 / (double)scale;
+        const float lift = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+        const float s = scale * lift, r = 1.0f / s;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float v = (float)((double)x[i] * inv);
+            const float xi = x[i] * lift, q = xi * r;
+            const float v = copysignf(fmaf(fmaf(-q, s, xi), r, q), q);  // (a remainder of 0 would turn -0 into 0)
             f[i] = v > 448.0f ? 448.0f : v < -448.0f ? -448.0f : v;  // keeps a NaN
         }
     }
     return pack8_e4m3(f);
+}
+
+// 8 bytes with the nontemporal hint.
+__device__ __forceinline__ void store_stream8(void* p, const uint2& v) {
+    typedef unsigned u2v __attribute__((ext_vector_type(2)));
+    u2v t;
+    t.x = v.x;
+    t.y = v.y;
+    __builtin_nontemporal_store(t, static_cast<u2v*>(p));
 }
 
 __device__ __forceinline__ void load_offsets(uint32_t* s_off, const uint32_t* off, int G) {
@@ -69,11 +87,10 @@ __device__ __forceinline__ void load_offsets(uint32_t* s_off, const uint32_t* of
 }
 
 // ---------------------------------------------------------------------------
-// Rows of bf16.  A unit is a row's segment of NC 512-element chunks; waves are
-// persistent and load the next unit while they encode the current one.
+// Rows of bf16.  A unit is a row's segment of kNC 512-element chunks.
 // SCATTER: unit rows are tokens, encoded once and stored to the rows of the
 // token's slots (top_k <= 64: lane k holds slot k).
-constexpr int kNC = 4;
+constexpr int kNC = 2;
 
 template <bool SCATTER>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t nrow,
@@ -92,14 +109,12 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
         const int64_t e0 = (u - r * nseg) * (kNC * kChunk) + lane * 8;
 #pragma unroll
         for (int c = 0; c < kNC; ++c)
-            v[c] = u < units && e0 + c * kChunk < K ? load_stream16(x + r * K + e0 + c * kChunk)
+            v[c] = e0 + c * kChunk < K ? load_stream16(x + r * K + e0 + c * kChunk)
                                                     : make_uint4(0, 0, 0, 0);
     };
-    uint4 v[kNC], vn[kNC];
-    int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave;
-    load(u, v);
-    for (; u < units; u += step) {
-        load(u + step, vn);
+    uint4 v[kNC];
+    for (int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave; u < units; u += step) {
+        load(u, v);
         const int64_t r = u / nseg;
         const int64_t e0 = (u - r * nseg) * (kNC * kChunk) + lane * 8;
         int32_t mine = -1;
@@ -133,8 +148,6 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
                 store(r);
             }
         }
-#pragma unroll
-        for (int c = 0; c < kNC; ++c) v[c] = vn[c];
     }
 }
 
@@ -143,7 +156,9 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
 // tile held in registers between the maximum and the encoding.  The transposed
 // codes go through LDS as words of four columns; a thread gathers four columns
 // of 16 rows and turns 4 x 4 byte blocks round with byte permutes, so both
-// layouts leave in 16-byte (plain: 8-byte) pieces of whole 128-byte lines.
+// layouts leave in 16-byte (plain: 8-byte) pieces of whole 128-byte lines.  Of
+// the two output streams the transposed one is stored nontemporally: 8 x 4096 x
+// 7168 in both layouts 148 us (6.3 TB/s), 182 with neither or both so.
 constexpr int kPitch = 33;  // words a tile row in LDS (32 and one against bank conflicts)
 
 __global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16_t* __restrict__ w, int64_t E,
@@ -218,8 +233,7 @@ __global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16
             for (int c = 0; c < 4; ++c) {
                 const int64_t k = k0 + 4 * kw + c;
                 if (k < K && n0 + nr < N)  // N is a multiple of 32: the 16 rows are all in or all out
-                    *reinterpret_cast<uint4*>(qt + (e * K + k) * N + n0 + nr) =
-                        make_uint4(o[c][0], o[c][1], o[c][2], o[c][3]);
+                    store_stream16(qt + (e * K + k) * N + n0 + nr, make_uint4(o[c][0], o[c][1], o[c][2], o[c][3]));
             }
         }
         // the next tile writes s_max before its first barrier and s_tile after it
@@ -249,16 +263,14 @@ __global__ __launch_bounds__(kThreads) void silu_quantize_kernel(const uint16_t*
     const int64_t units = T * nseg, step = (int64_t)gridDim.x * kWavesPerBlock, nblk = (I + kBlk - 1) / kBlk;
     auto load = [&](int64_t u, uint4 (&v)[2]) {
         const int64_t r = u / nseg, j = (u - r * nseg) * kChunk + lane * 8;
-        const bool in = u < units && j < I;
+        const bool in = j < I;
         const uint16_t* p = h + r * 2 * I + 2 * j;
 #pragma unroll
         for (int c = 0; c < 2; ++c) v[c] = in ? load_stream16(p + 8 * c) : make_uint4(0, 0, 0, 0);
     };
-    uint4 v[2], vn[2];
-    int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave;
-    load(u, v);
-    for (; u < units; u += step) {
-        load(u + step, vn);
+    uint4 v[2];
+    for (int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave; u < units; u += step) {
+        load(u, v);
         const int64_t r = u / nseg, j = (u - r * nseg) * kChunk + lane * 8;
         if (wave_row_covered(s_off, G, T, r)) {
             float gu[16], y[8];
@@ -269,17 +281,16 @@ __global__ __launch_bounds__(kThreads) void silu_quantize_kernel(const uint16_t*
             const float sc = amax_of16(amax8(y)) / 448.0f;
             const uint2 p = encode8(y, sc);
             if (j < I) {
-                *reinterpret_cast<uint2*>(q + r * I + j) = p;
+                store_stream8(q + r * I + j, p);
                 if ((lane & 15) == 0) scales[r * nblk + j / kBlk] = sc;
             }
         }
-        v[0] = vn[0];
-        v[1] = vn[1];
     }
 }
 
 // The gradient: a lane's 8 outputs give 16 elements of dh, so 8 lanes are a
-// block of dh.  dh may be h itself: a lane has read its elements before it
+// block of dh.  dh leaves nontemporally, the codes do not (32768 x 2048: 146 us,
+// with both streams so 164).  dh may be h itself: a lane has read its elements before it
 // writes them, and no other lane reads them.
 template <bool KEEP, bool QUANT>
 __global__ __launch_bounds__(kThreads) void silu_backward_kernel(const uint16_t* h, const uint16_t* __restrict__ dy,
@@ -294,17 +305,15 @@ __global__ __launch_bounds__(kThreads) void silu_backward_kernel(const uint16_t*
     const int64_t units = T * nseg, step = (int64_t)gridDim.x * kWavesPerBlock, nblk = (2 * I + kBlk - 1) / kBlk;
     auto load = [&](int64_t u, uint4 (&v)[3]) {
         const int64_t r = u / nseg, j = (u - r * nseg) * kChunk + lane * 8;
-        const bool in = u < units && j < I;
+        const bool in = j < I;
         const uint16_t* p = h + r * 2 * I + 2 * j;
         v[0] = in ? load_stream16(p) : make_uint4(0, 0, 0, 0);
         v[1] = in ? load_stream16(p + 8) : make_uint4(0, 0, 0, 0);
         v[2] = in ? load_stream16(dy + r * I + j) : make_uint4(0, 0, 0, 0);
     };
-    uint4 v[3], vn[3];
-    int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave;
-    load(u, v);
-    for (; u < units; u += step) {
-        load(u + step, vn);
+    uint4 v[3];
+    for (int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave; u < units; u += step) {
+        load(u, v);
         const int64_t r = u / nseg, j = (u - r * nseg) * kChunk + lane * 8;
         if (wave_row_covered(s_off, G, T, r)) {
             float gu[16], d[8], o[16];
@@ -340,25 +349,13 @@ __global__ __launch_bounds__(kThreads) void silu_backward_kernel(const uint16_t*
                 }
             }
         }
-#pragma unroll
-        for (int c = 0; c < 3; ++c) v[c] = vn[c];
     }
 }
 
-// Persistent launch: workgroups that stay resident (8 a CU), or as many as have work.
-unsigned resident_grid(int64_t units) {
-    static thread_local int cached_device = -1, cached_cus = 0;
-    int dev = 0;
-    if (hipGetDevice(&dev) == hipSuccess && dev != cached_device) {
-        int cus = 0;
-        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess) {
-            cached_device = dev;
-            cached_cus = cus;
-        }
-    }
-    const int64_t cap = (int64_t)(cached_cus > 0 ? cached_cus : 256) * 8;
+// A wave per unit; a launch holds fewer than 2^32 threads, past this many workgroups they loop.
+unsigned grid_of(int64_t units) {
     const int64_t blocks = (units + kWavesPerBlock - 1) / kWavesPerBlock;
-    return (unsigned)(blocks < cap ? blocks : cap);
+    return (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
 }
 
 }  // namespace
@@ -367,7 +364,7 @@ hipError_t launch_quantize_block128(const void* x, int64_t ntok, const int32_t* 
                                     float* scales, const uint32_t* off, int G, int64_t T, int64_t K,
                                     hipStream_t stream) {
     const int64_t nseg = (K + kNC * kChunk - 1) / (kNC * kChunk);
-    const dim3 grid(resident_grid(ntok * nseg));
+    const dim3 grid(grid_of(ntok * nseg));
     if (row_of_slot)
         hipLaunchKernelGGL(quantize_rows_kernel<true>, grid, dim3(kThreads), 0, stream,
                            static_cast<const uint16_t*>(x), ntok, row_of_slot, top_k, static_cast<uint8_t*>(q),
@@ -392,7 +389,7 @@ hipError_t launch_quantize_weights_block128(const void* w, int64_t E, int64_t N,
 hipError_t launch_silu_quantize_block128(const void* h, void* yq, float* ys, const uint32_t* off, int G, int64_t T,
                                          int64_t I, hipStream_t stream) {
     const int64_t nseg = (I + kChunk - 1) / kChunk;
-    hipLaunchKernelGGL(silu_quantize_kernel, dim3(resident_grid(T * nseg)), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL(silu_quantize_kernel, dim3(grid_of(T * nseg)), dim3(kThreads), 0, stream,
                        static_cast<const uint16_t*>(h), static_cast<uint8_t*>(yq), ys, off, G, T, I, (int)nseg);
     return hipGetLastError();
 }
@@ -400,7 +397,7 @@ hipError_t launch_silu_quantize_block128(const void* h, void* yq, float* ys, con
 hipError_t launch_silu_backward_block128(const void* h, const void* dy, void* dh, void* dh_q, float* dh_scales,
                                          const uint32_t* off, int G, int64_t T, int64_t I, hipStream_t stream) {
     const int64_t nseg = (I + kChunk - 1) / kChunk;
-    const dim3 grid(resident_grid(T * nseg));
+    const dim3 grid(grid_of(T * nseg));
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, static_cast<const uint16_t*>(h),
                            static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(dh), static_cast<uint8_t*>(dh_q),

@@ -83,21 +83,24 @@ def test_quantize_rows(T, K):
     assert np.array_equal(q_g.numpy(), q)
 
 
-def test_quantize_every_quotient():
-    """Every bf16 magnitude up to the block's maximum, under maxima of every
-    mantissa in several binades: the codes of IEEE division."""
-    for top in (0x3F80, 0x0080, 0x7F00, 0x4300, 0x2000):
-        rows = []
-        for m in range(0, 128, 3):
-            amax = top + m
-            vals = np.arange(max(0, amax - 1270), amax + 1, 10, dtype=np.uint16)[-127:]
-            rows.append(np.concatenate([vals, np.full(B - vals.size, amax, np.uint16)]))
-        xb = np.stack(rows)
-        x = bf16_values(xb).astype(np.float32).reshape(xb.shape)
-        q, s = ref_rows(x)
-        got_q, got_s = mxg.quantize_block128(to_gpu(xb.view(np.int16)).view(torch.bfloat16),
-                                             offsets_gpu(np.array([0, len(rows)], np.uint32)))
-        assert np.array_equal(got_s.cpu().numpy(), s) and np.array_equal(got_q.cpu().numpy(), q), hex(top)
+@pytest.mark.parametrize("exponent", [1, 20, 66, 67, 100, 127, 200, 254])
+def test_quantize_every_quotient(exponent):
+    """Every bf16 magnitude of the ten binades below a block's maximum (below that
+    the codes are 0), under maxima of every mantissa, in binades from the smallest
+    normals to the largest: the codes of IEEE division, bit for bit."""
+    rows = []
+    for m in range(128):
+        amax = (exponent << 7) | m
+        vals = np.arange(max(0, amax - 1280), amax + 1)
+        vals = np.concatenate([vals, np.full(-len(vals) % 127, amax)]).reshape(-1, 127)
+        rows.append(np.concatenate([vals, np.full((len(vals), 1), amax)], 1))
+    xb = np.concatenate(rows).astype(np.uint16)
+    xb[1::2] |= 0x8000  # both signs
+    x = bf16_values(xb).astype(np.float32).reshape(xb.shape)
+    q, s = ref_rows(x)
+    got_q, got_s = mxg.quantize_block128(to_gpu(xb.view(np.int16)).view(torch.bfloat16),
+                                         offsets_gpu(np.array([0, len(xb)], np.uint32)))
+    assert np.array_equal(got_s.cpu().numpy(), s) and np.array_equal(got_q.cpu().numpy(), q)
 
 
 def test_quantize_uncovered_rows_stay():
