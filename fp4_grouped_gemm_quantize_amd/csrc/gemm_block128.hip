@@ -66,6 +66,44 @@ __device__ __forceinline__ void lds_dma4(const void* base_in, uint32_t voff, uin
         : "memory");
 }
 
+// N direct-to-LDS loads of 16 bytes per lane, load j to lds + 1024 NW j (the lanes
+// of this wave side by side), in one block: the first s_nop gives a base written
+// by a vector instruction its wait states, the others M0 its own.
+template <int N, int STRIDE>
+__device__ __forceinline__ void lds_dma16_rows(const void* base_in, const uint32_t (&off)[N], uint32_t lds_in) {
+    const uint64_t b = (uint64_t)base_in;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    const uint64_t base = ((uint64_t)hi << 32) | (uint64_t)lo;
+    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(lds_in);
+    static_assert(N == 1 || N == 2 || N == 4, "loads per block");
+    if constexpr (N == 1)
+        __asm__ volatile(
+            "s_mov_b32 m0, %2\n\ts_nop 4\n\t"
+            "global_load_lds_dwordx4 %0, %1"
+            :
+            : "v"(off[0]), "s"(base), "s"(lds)
+            : "memory", "m0");
+    else if constexpr (N == 2)
+        __asm__ volatile(
+            "s_mov_b32 m0, %3\n\ts_nop 4\n\t"
+            "global_load_lds_dwordx4 %0, %2\n\ts_add_u32 m0, m0, %4\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %1, %2"
+            :
+            : "v"(off[0]), "v"(off[1]), "s"(base), "s"(lds), "n"(STRIDE)
+            : "memory", "m0", "scc");
+    else
+        __asm__ volatile(
+            "s_mov_b32 m0, %5\n\ts_nop 4\n\t"
+            "global_load_lds_dwordx4 %0, %4\n\ts_add_u32 m0, m0, %6\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %1, %4\n\ts_add_u32 m0, m0, %6\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %2, %4\n\ts_add_u32 m0, m0, %6\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %3, %4"
+            :
+            : "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base), "s"(lds), "n"(STRIDE)
+            : "memory", "m0", "scc");
+}
+
 __device__ __forceinline__ v4f mma128(const v8i& n, const v8i& t) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, t, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
@@ -168,34 +206,40 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     const int chunk = swz_chunk<kSB>(r0, lane % 8);   // 16-byte piece it fetches: the swizzle
     const int ring0 = (int)lds_addr(s_ring), scl0 = (int)lds_addr(s_scl);
     uint32_t a_off[A_J], b_off[B_J];
+    const uint8_t *p_a = nullptr, *p_b = nullptr;  // the tile's operands at the producer's stage
     auto set_tile = [&]() {
+        p_a = args.a + pc.m0 * K;
+        p_b = args.b + ((int64_t)pc.e * args.N + pc.n0) * K;
         // rows past the group and columns past N re-read the last real one
 #pragma unroll
         for (int j = 0; j < A_J; ++j) {
             const int r = r0 + 8 * NW * j;
-            a_off[j] = (uint32_t)(r < pc.rows_in ? r : pc.rows_in - 1) * (uint32_t)K;
+            a_off[j] = (uint32_t)(r < pc.rows_in ? r : pc.rows_in - 1) * (uint32_t)K + chunk * 16;
         }
 #pragma unroll
         for (int j = 0; j < B_J; ++j) {
             const int r = r0 + 8 * NW * j;
-            b_off[j] = (uint32_t)(r < pc.cols_in ? r : pc.cols_in - 1) * (uint32_t)K;
+            b_off[j] = (uint32_t)(r < pc.cols_in ? r : pc.cols_in - 1) * (uint32_t)K + chunk * 16;
         }
     };
     // Issue the producer's next stage; returns the number of loads this wave issued.
     auto produce = [&]() -> int {
         if (pw >= ws.items) return 0;
         if (pk == 0) set_tile();
-        const int64_t kb = (int64_t)pk * kSB;
-        const uint8_t* ak = args.a + pc.m0 * K + kb;
-        const uint8_t* bk = args.b + ((int64_t)pc.e * args.N + pc.n0) * K + kb;
-        // pieces past the end of K (last stage) fetch the stage's first one
-        // instead; the consumer zeroes them
-        const uint32_t c16 = kb + chunk * 16 < K ? chunk * 16 : 0;
-        const int slot = ring0 + pslot * kStage;
+        if (pk == nkt - 1 && K % kSB != 0) {
+            // pieces past the end of K fetch the stage's first one instead; the consumer zeroes them
+            const uint32_t back = (int64_t)pk * kSB + chunk * 16 < K ? 0 : chunk * 16;
 #pragma unroll
-        for (int j = 0; j < A_J; ++j) lds_dma16<false>(ak, a_off[j] + c16, slot + (wave + NW * j) * 1024);
+            for (int j = 0; j < A_J; ++j) a_off[j] -= back;
 #pragma unroll
-        for (int j = 0; j < B_J; ++j) lds_dma16<false>(bk, b_off[j] + c16, slot + kAStage + (wave + NW * j) * 1024);
+            for (int j = 0; j < B_J; ++j) b_off[j] -= back;
+        }
+        // (the A loads end where the B loads begin: kAStage is A_J loads of every wave)
+        const int slot = ring0 + pslot * kStage + wave * 1024;
+        lds_dma16_rows<A_J, NW * 1024>(p_a, a_off, slot);
+        lds_dma16_rows<B_J, NW * 1024>(p_b, b_off, slot + kAStage);
+        p_a += kSB;
+        p_b += kSB;
         int issued = A_J + B_J;
         if (pk % kSclBlocks == 0) {
             pchunk = pchunk + 1 < kSlots ? pchunk + 1 : 0;
