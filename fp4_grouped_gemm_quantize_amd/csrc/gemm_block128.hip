@@ -223,7 +223,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         }
     };
     // Issue the producer's next stage; returns the number of loads this wave issued.
-    auto produce = [&]() -> int {
+    auto produce_issue = [&]() -> int {
         if (pw >= ws.items) return 0;
         if (pk == 0) set_tile();
         if (pk == nkt - 1 && K % kSB != 0) {
@@ -261,13 +261,16 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
                      (brow * (uint32_t)nkt + col) * 4, dst + kSclA);
             issued += S_J + 1;
         }
+        return issued;
+    };
+    auto produce_next = [&]() {
+        if (pw >= ws.items) return;
         pslot = pslot + 1 < kSlots ? pslot + 1 : 0;
         if (++pk == nkt) {
             pk = 0;
             pw += gridDim.x;
             next_item(pw, pc);
         }
-        return issued;
     };
     constexpr int L = A_J + B_J;
 
@@ -275,7 +278,17 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     int64_t cw = pw;
     Coord cc = pc;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) produce();
+    for (int i = 0; i < kAhead; ++i) {
+        produce_issue();
+        produce_next();
+    }
+    // Waves w and w + 4 share a SIMD.  The upper half issues its loads of a stage
+    // behind its first products instead of before its fragment reads, so that one
+    // wave of a SIMD multiplies while the other issues loads and waits for its
+    // fragments (256-row tiles 520 -> 507 us on 65536 uneven rows, 128-row tiles
+    // 28.7 -> 27.1 us on 5003; behind the 8th product 532, all waves so 554).
+    constexpr int kLate = 3;
+    const bool late = NW == 8 && wave >= NW / 2;
     stage_barrier<0>();
     int cslot = 0, cchunk = 0;
     // fragment addresses inside a slot: row l16 of the wave's first 16, pieces kg and kg + 4
@@ -293,7 +306,8 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         for (int kt = 0; kt < nkt; ++kt) {
             const uint8_t* cur = s_ring + cslot * kStage;
             if (kt % kSclBlocks == 0) cchunk = cchunk + 1 < kSlots ? cchunk + 1 : 0;
-            const int issued = produce();
+            int issued = 0;
+            if (!late || !wave_live) issued = produce_issue();
             if (kt == nkt - 1 && K % kSB != 0) {
                 // the pieces past the end of K hold other bytes: zero them
                 const int good = (int)(K % kSB) / 16;
@@ -336,6 +350,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
                         const int i = q / TM, j = q % TM;
                         part[q % (kLag + 1)] = mma128(nf[i & 1], tf[j]);
                         __builtin_amdgcn_sched_barrier(0);
+                        if (q == kLate && late) issued = produce_issue();
                         if (j == TM - 1 && i + 2 < TN) nf[i & 1] = frag(fb + (i + 2) * 16 * kSB);
                         if (q < TM) s[q] *= sb;
                     }
@@ -348,6 +363,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
                     __builtin_amdgcn_sched_barrier(0);  // keep the steps in this order
                 }
             }
+            produce_next();
             // the next stage must have landed; those issued after it may stay in flight
             if (kAhead == 1 || drain || issued == 0) stage_barrier<0>();
             else if (issued == L) stage_barrier<L>();
