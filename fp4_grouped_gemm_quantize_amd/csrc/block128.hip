@@ -8,11 +8,12 @@
 // All are HBM-bound streams read once and written once.  16 lanes x 8 elements
 // form a 1 x 128 block, so a wave's 16-byte loads stay contiguous and the block
 // maximum is four register exchanges.  Every wave takes one unit of work and
-// ends: where half the bytes are writes, persistent waves that load the next
-// unit while they encode the current one were slower at every grid size (SwiGLU
-// gradient of 32768 x 2048: 179 us with 8 resident workgroups a CU, 156 with 4,
-// 161 with 64, 146 so, 5.5 TB/s; scattered quantize of 8192 x 4096 to 65536
-// rows: 66, 66, 59, 59 us).
+// ends: persistent waves that load the next unit while they encode the current
+// one were slower at every grid size (SwiGLU gradient of 32768 x 2048, inputs in
+// the last-level cache: 179 us with 8 resident workgroups a CU, 156 with 4, 161
+// with 64, 147 so).  Which streams carry the nontemporal hint is by measurement
+// on inputs that no cache holds, and stated at each kernel; the times there are
+// of such inputs too.
 #include "mxg_device.h"
 #include "mxg_internal.h"
 
@@ -87,7 +88,9 @@ __device__ __forceinline__ void load_offsets(uint32_t* s_off, const uint32_t* of
 }
 
 // ---------------------------------------------------------------------------
-// Rows of bf16.  A unit is a row's segment of kNC 512-element chunks.
+// Rows of bf16.  A unit is a row's segment of kNC 512-element chunks; loads and
+// codes are nontemporal (8192 x 4096 scattered to 65536 rows: 69 us, 5.0 TB/s; 72
+// with ordinary stores).
 // SCATTER: unit rows are tokens, encoded once and stored to the rows of the
 // token's slots (top_k <= 64: lane k holds slot k).
 constexpr int kNC = 2;
@@ -135,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
                 for (int c = 0; c < kNC; ++c) {
                     const int64_t e = e0 + c * kChunk;
                     if (e >= K) continue;
-                    *reinterpret_cast<uint2*>(q + t * K + e) = pk[c];
+                    store_stream8(q + t * K + e, pk[c]);
                     if ((lane & 15) == 0) scales[t * nblk + e / kBlk] = sc[c];
                 }
             };
@@ -156,9 +159,9 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
 // tile held in registers between the maximum and the encoding.  The transposed
 // codes go through LDS as words of four columns; a thread gathers four columns
 // of 16 rows and turns 4 x 4 byte blocks round with byte permutes, so both
-// layouts leave in 16-byte (plain: 8-byte) pieces of whole 128-byte lines.  Of
-// the two output streams the transposed one is stored nontemporally: 8 x 4096 x
-// 7168 in both layouts 148 us (6.3 TB/s), 182 with neither or both so.
+// layouts leave in 16-byte (plain: 8-byte) pieces of whole 128-byte lines, both
+// nontemporal: 8 x 4096 x 7168 in both layouts 178 us (5.3 TB/s), 185 with either
+// or neither so.
 constexpr int kPitch = 33;  // words a tile row in LDS (32 and one against bank conflicts)
 
 __global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16_t* __restrict__ w, int64_t E,
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16
             float f[8];
             unpack8(v[i], f);
             const uint2 p = encode8(f, sc);
-            if (in_k && n < N) *reinterpret_cast<uint2*>(q + (e * N + n) * K + k0 + c8) = p;
+            if (in_k && n < N) store_stream8(q + (e * N + n) * K + k0 + c8, p);
             if (qt) {
                 s_tile[r * kPitch + c8 / 4] = p.x;
                 s_tile[r * kPitch + c8 / 4 + 1] = p.y;
@@ -251,7 +254,8 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
 }
 
 // A unit is 512 outputs of a row: a lane's 8 outputs are 16 of h (two 16-byte
-// loads), 16 lanes a block.
+// loads), 16 lanes a block; all nontemporal (32768 x 2048: 68 us, 4.9 TB/s; 72
+// with ordinary stores).
 __global__ __launch_bounds__(kThreads) void silu_quantize_kernel(const uint16_t* __restrict__ h,
                                                                  uint8_t* __restrict__ q, float* __restrict__ scales,
                                                                  const uint32_t* __restrict__ off, int G, int64_t T,
@@ -289,8 +293,8 @@ __global__ __launch_bounds__(kThreads) void silu_quantize_kernel(const uint16_t*
 }
 
 // The gradient: a lane's 8 outputs give 16 elements of dh, so 8 lanes are a
-// block of dh.  dh leaves nontemporally, the codes do not (32768 x 2048: 146 us,
-// with both streams so 164).  dh may be h itself: a lane has read its elements before it
+// block of dh.  No stream is nontemporal (32768 x 2048, dh kept and quantised:
+// 144 us, 5.6 TB/s; 149 with the loads so, 157 with dh too, 166 with all).  dh may be h itself: a lane has read its elements before it
 // writes them, and no other lane reads them.
 template <bool KEEP, bool QUANT>
 __global__ __launch_bounds__(kThreads) void silu_backward_kernel(const uint16_t* h, const uint16_t* __restrict__ dy,
@@ -307,9 +311,9 @@ __global__ __launch_bounds__(kThreads) void silu_backward_kernel(const uint16_t*
         const int64_t r = u / nseg, j = (u - r * nseg) * kChunk + lane * 8;
         const bool in = j < I;
         const uint16_t* p = h + r * 2 * I + 2 * j;
-        v[0] = in ? load_stream16(p) : make_uint4(0, 0, 0, 0);
-        v[1] = in ? load_stream16(p + 8) : make_uint4(0, 0, 0, 0);
-        v[2] = in ? load_stream16(dy + r * I + j) : make_uint4(0, 0, 0, 0);
+        v[0] = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+        v[1] = in ? *reinterpret_cast<const uint4*>(p + 8) : make_uint4(0, 0, 0, 0);
+        v[2] = in ? *reinterpret_cast<const uint4*>(dy + r * I + j) : make_uint4(0, 0, 0, 0);
     };
     uint4 v[3];
     for (int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave; u < units; u += step) {
@@ -336,7 +340,7 @@ __global__ __launch_bounds__(kThreads) void silu_backward_kernel(const uint16_t*
                         w[c].y = f32x2_to_bf16x2(o[8 * c + 2], o[8 * c + 3]);
                         w[c].z = f32x2_to_bf16x2(o[8 * c + 4], o[8 * c + 5]);
                         w[c].w = f32x2_to_bf16x2(o[8 * c + 6], o[8 * c + 7]);
-                        store_stream16(dh + r * 2 * I + 2 * j + 8 * c, w[c]);
+                        *reinterpret_cast<uint4*>(dh + r * 2 * I + 2 * j + 8 * c) = w[c];
                     }
                 }
             }

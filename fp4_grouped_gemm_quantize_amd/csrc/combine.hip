@@ -93,7 +93,8 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __res
 
 // The permutation, token-major: a wave reads one segment of a token's row once
 // and stores it to the row of each of the token's slots (read once per slot the
-// same rows would cross the fabric top_k times).  Bound by the stores.
+// same rows would cross the fabric top_k times).  Bound by the stores: 8192 x 8
+// rows of 4096 122 us, 5.0 TB/s of which eight ninths are writes.
 constexpr int kSeg = 4;  // 16-byte vectors per lane per segment: 2048 elements a wave
 
 __global__ __launch_bounds__(kThreads) void permute_kernel(const uint16_t* __restrict__ x, int64_t ntok, int64_t H,
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(const uint16_t* __res
 
 // The permutation's gradient: each token's row is the sum of its slots' rows,
 // in slot order, in fp32.  A wave sums one 512-element piece of a token's row,
-// so few tokens still fill the chip.
+// so few tokens still fill the chip (4096 x 8 rows of 7168: 98 us, 5.4 TB/s).
 __global__ __launch_bounds__(kThreads) void permute_backward_kernel(const uint16_t* __restrict__ drows, int64_t T,
                                                                     int64_t H, int nseg,
                                                                     const int32_t* __restrict__ row_of_slot,
@@ -172,6 +173,7 @@ __global__ __launch_bounds__(kThreads) void permute_backward_kernel(const uint16
 // into the slot's row and takes its dot product with the slot's y row (fp32 per
 // lane, then over the wave, then over the waves: a fixed order).  Consecutive
 // slots go to one XCD, so a token's row is fetched into one L2 for all of them.
+// 4096 x 8 rows of 7168: 186 us, 5.4 TB/s (208 with ordinary stores).
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, int64_t T, int64_t H,
     const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights, int64_t nslots, int top_k,
