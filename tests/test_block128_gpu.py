@@ -296,6 +296,17 @@ def test_gemm_many_groups():
     check_gemm(int(off[-1]), 7, 136, 160, off, rng.integers(0, 7, G))
 
 
+@pytest.mark.parametrize("most,N,K", [(128, 256, 160), (391, 512, 32)])
+def test_gemm_many_groups_of_larger_tiles(most, N, K):
+    """As many groups as there may be, of 0 to `most` rows: the 128- and the 256-row tiles."""
+    rng = np.random.default_rng(most)
+    G = 1024
+    sizes = rng.integers(0, most + 1, G)
+    sizes[[0, 1, G - 1]] = 0, 1, 0
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    check_gemm(int(off[-1]) + 5, 7, N, K, off, rng.integers(0, 7, G))
+
+
 @pytest.mark.parametrize("hint", [0, 1, 64, 1 << 20, 1 << 62])
 def test_gemm_hint(hint):
     check_gemm(150, 5, 264, 512, [0, 10, 20, 140, 150], [0, 1, 2, 3], hint=hint)
