@@ -51,8 +51,8 @@ EXPORTED = ("mx_grouped_quantize", "mx_grouped_quantize_gather", "mx_grouped_qua
             "mx_prepare_weights_fp8", "mx_grouped_matmul_prepared", "mx_moe_topk", "mx_moe_topk_backward",
             "mx_moe_sort", "mx_moe_permute", "mx_moe_permute_backward", "mx_moe_combine_backward",
             "mx_grouped_quantize_block128", "mx_grouped_quantize_block128_scatter", "mx_quantize_weights_block128",
-            "mx_grouped_matmul_block128", "mx_silu_quantize_block128", "mx_silu_backward_block128", "mxg_clock_probe", "mxg_fp8_tile",
-            "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
+            "mx_grouped_matmul_block128", "mx_silu_quantize_block128", "mx_silu_backward_block128", "mxg_clock_probe",
+            "mxg_fp8_tile", "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
 
 
 class MxgError(RuntimeError):
@@ -802,11 +802,10 @@ def _top_k(row_of_slot, num_tokens: int, dev) -> int:
 
 
 def _apart(a, b, names: str) -> None:
-    """Refuse two tensors that share memory."""
-    if a.numel() and b.numel():
-        a0, b0 = a.data_ptr(), b.data_ptr()
-        if a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size():
-            raise ValueError(f"{names} may not overlap")
+    """Refuse two tensors that share memory (an empty one has no address)."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    if a0 < b0 + b.nbytes and b0 < a0 + a.nbytes:
+        raise ValueError(f"{names} may not overlap")
 
 
 def mx_moe_topk(score: int, logits, topk_ids, topk_weights, bias=None, renormalize: bool = True,
@@ -838,6 +837,8 @@ def mx_moe_topk_backward(score: int, logits, topk_ids, dweights, dlogits, renorm
         raise ValueError(f"topk_ids: {rows} rows, expected {S}")
     _expect(dweights, "dweights", _F32, (S, k), dev)
     _expect(dlogits, "dlogits", (logits.dtype,), (S, E), dev)
+    _apart(dlogits, logits, "dlogits and logits")
+    _apart(dlogits, dweights, "dlogits and dweights")
     _run("mx_moe_topk_backward", dev, F32 if logits.dtype == torch.float32 else BF16, score, logits.data_ptr(),
          topk_ids.data_ptr(), dweights.data_ptr(), S, E, k, 1 if renormalize else 0, scale, dlogits.data_ptr())
 
@@ -850,8 +851,10 @@ def mx_moe_sort(topk_ids, row_offsets, row_of_slot, slot_of_row) -> None:
     E = _groups(row_offsets, dev)
     _expect(row_of_slot, "row_of_slot", _I32T, (S * k,), dev)
     _expect(slot_of_row, "slot_of_row", _I32T, (S * k,), dev)
-    _run("mx_moe_sort", dev, topk_ids.data_ptr(), S, k, E, row_offsets.data_ptr(), row_of_slot.data_ptr(),
-         slot_of_row.data_ptr())
+    ids, ros, sor, n = topk_ids.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(), 4 * S * k
+    if -n < ids - ros < n or -n < ids - sor < n or -n < ros - sor < n:
+        raise ValueError("topk_ids, row_of_slot and slot_of_row may not overlap")
+    _run("mx_moe_sort", dev, ids, S, k, E, row_offsets.data_ptr(), ros, sor)
 
 
 def mx_moe_permute(x, row_of_slot, rows) -> None:
@@ -894,6 +897,7 @@ def mx_moe_combine_backward(dout, y, row_of_slot, weights, dy, dweights) -> None
         raise ValueError("weights and dweights must hold num_tokens * top_k entries")
     _apart(dy, y, "dy and y")
     _apart(dy, dout, "dy and dout")
+    _apart(weights, dweights, "weights and dweights")
     _run("mx_moe_combine_backward", dev, dout.data_ptr(), y.data_ptr(), T, H, row_of_slot.data_ptr(),
          weights.data_ptr(), S, k, dy.data_ptr(), dweights.data_ptr())
 

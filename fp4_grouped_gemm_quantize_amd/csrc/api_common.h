@@ -11,6 +11,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <exception>
 #include <vector>
 
 namespace mxg {
@@ -63,18 +64,22 @@ inline mxg_status check_routing(const uint32_t* off, const int32_t* ids, int64_t
                          hipStream_t stream) {
     if (!validation_on()) return MXG_SUCCESS;
     t_validation_msg[0] = '\0';
-    std::vector<uint32_t> h_off((size_t)G + 1);
-    std::vector<int32_t> h_ids(ids != nullptr && E > 0 ? (size_t)G : 0);
-    if (hipMemcpyAsync(h_off.data(), off, sizeof(uint32_t) * h_off.size(), hipMemcpyDeviceToHost, stream) !=
-        hipSuccess)
-        return MXG_ERROR_LAUNCH;
-    if (!h_ids.empty() && hipMemcpyAsync(h_ids.data(), ids, sizeof(int32_t) * h_ids.size(), hipMemcpyDeviceToHost,
-                                         stream) != hipSuccess)
-        return MXG_ERROR_LAUNCH;
-    if (hipStreamSynchronize(stream) != hipSuccess) return MXG_ERROR_LAUNCH;
-    if (find_violation(h_off.data(), h_ids.empty() ? nullptr : h_ids.data(), G, E, T, t_validation_msg,
-                       sizeof t_validation_msg))
-        return MXG_ERROR_INVALID_VALUE;
+    try {
+        std::vector<uint32_t> h_off((size_t)G + 1);
+        std::vector<int32_t> h_ids(ids != nullptr && E > 0 ? (size_t)G : 0);
+        if (hipMemcpyAsync(h_off.data(), off, sizeof(uint32_t) * h_off.size(), hipMemcpyDeviceToHost, stream) !=
+            hipSuccess)
+            return MXG_ERROR_LAUNCH;
+        if (!h_ids.empty() && hipMemcpyAsync(h_ids.data(), ids, sizeof(int32_t) * h_ids.size(), hipMemcpyDeviceToHost,
+                                             stream) != hipSuccess)
+            return MXG_ERROR_LAUNCH;
+        if (hipStreamSynchronize(stream) != hipSuccess) return MXG_ERROR_LAUNCH;
+        if (find_violation(h_off.data(), h_ids.empty() ? nullptr : h_ids.data(), G, E, T, t_validation_msg,
+                           sizeof t_validation_msg))
+            return MXG_ERROR_INVALID_VALUE;
+    } catch (const std::exception&) {
+        return MXG_ERROR_LAUNCH;  // no exception leaves an entry point
+    }
     return MXG_SUCCESS;
 }
 

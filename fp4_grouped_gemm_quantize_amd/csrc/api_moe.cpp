@@ -2,10 +2,8 @@
 // the 128-block FP8 format and their gradients: argument validation on the
 // host (before anything is enqueued), then one launch per call.  No
 // allocation outside the MXG_VALIDATE check, no host synchronisation outside
-// it, no state.
+// it, no state.  No exception leaves an entry point.
 #include "api_common.h"
-
-#include <new>
 
 using namespace mxg::api;
 
@@ -26,7 +24,7 @@ mxg_status check_distinct_rows(const int32_t* row_of_slot, int64_t nslots, int64
                 hipSuccess ||
             hipStreamSynchronize(stream) != hipSuccess)
             return MXG_ERROR_LAUNCH;
-        std::vector<bool> seen((size_t)T);
+        std::vector<bool> seen((size_t)(T < INT32_MAX ? T : (int64_t)INT32_MAX + 1));  // what an int32 can name
         for (int64_t i = 0; i < nslots; ++i) {
             const int64_t r = h[(size_t)i];
             if (r < 0 || r >= T) continue;
@@ -37,7 +35,7 @@ mxg_status check_distinct_rows(const int32_t* row_of_slot, int64_t nslots, int64
             }
             seen[(size_t)r] = true;
         }
-    } catch (const std::bad_alloc&) {
+    } catch (const std::exception&) {
         return MXG_ERROR_LAUNCH;
     }
     return MXG_SUCCESS;
@@ -52,7 +50,7 @@ mxg_status check_topk_sizes(int type, int score, int64_t ntok, int32_t E, int32_
 
 mxg_status check_rows_sizes(int64_t T, int64_t H, int64_t ntok, int32_t top_k) {
     if (H <= 0 || T < 0 || ntok < 0 || top_k < 1) return MXG_ERROR_INVALID_VALUE;
-    if (H % 8 != 0 || ntok > INT32_MAX / top_k) return MXG_ERROR_NOT_SUPPORTED;
+    if (H % 8 != 0 || H > INT32_MAX || ntok > INT32_MAX / top_k) return MXG_ERROR_NOT_SUPPORTED;
     return MXG_SUCCESS;
 }
 

@@ -99,6 +99,10 @@ int main() {
                "combine_backward");
         expect(mx_moe_combine_backward(buf, buf, 4, 8, twice, f, 2, 2, buf, f, nullptr), refused, kept,
                "combine_backward of repeated rows");
+        // more rows than an int32 can name, more than there is memory for: no exception leaves
+        expect(mx_moe_permute(buf, 2, 8, rows, 2, buf, INT64_MAX, nullptr), MXG_SUCCESS, 1, "permute into many rows");
+        expect(mx_moe_combine_backward(buf, buf, INT64_MAX, 8, twice, f, 2, 2, buf, f, nullptr), refused, kept,
+               "combine_backward of many rows, repeated");
         expect(mx_moe_combine_backward(buf, nullptr, 0, 8, rows, f, 2, 2, nullptr, f, nullptr), MXG_SUCCESS, 1,
                "combine_backward without rows");
         expect(mx_grouped_quantize_block128(buf, buf, f, off, 2, 4, 32, nullptr), MXG_SUCCESS, 1, "quantize");

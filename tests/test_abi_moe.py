@@ -133,6 +133,14 @@ def test_both_gradient_outputs_missing():
     assert mxg.lib().mx_silu_backward_block128(*good) == INVALID
 
 
+@pytest.mark.parametrize("name,at", [("mx_moe_permute", 2), ("mx_moe_permute_backward", 2),
+                                     ("mx_moe_combine_backward", 3)])
+def test_rows_too_long(name, at):
+    args = list(CASES[name][0])
+    args[at] = 2 ** 31
+    assert getattr(mxg.lib(), name)(*args) == UNSUPPORTED
+
+
 def test_binding_refuses_wrong_tensors():
     """dtype, shape and device are checked before the library is called."""
     x = torch.zeros((4, 64), dtype=torch.bfloat16)

@@ -374,6 +374,23 @@ def test_combine_gradient_against_differences():
     assert abs((dw64 * vw).sum() - num_w) <= (np.abs(dw64 * vw)).sum() * 40 * 2.0 ** -24 + 1e-3
 
 
+def test_outputs_over_inputs_are_refused():
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    a, b = torch.zeros((2, 8), dtype=torch.int32, device="cuda")
+    x = torch.zeros((4, 2), device="cuda")
+    y, d = torch.zeros((2, 4, 8), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(8, device="cuda")
+    for call in (lambda: mxg.mx_moe_sort(ids, off, ids.view(-1), b), lambda: mxg.mx_moe_sort(ids, off, a, ids.view(-1)),
+                 lambda: mxg.mx_moe_sort(ids, off, a, a), lambda: mxg.mx_moe_topk_backward(SOFTMAX, x, ids, w.view(4, 2), x),
+                 lambda: mxg.mx_moe_topk_backward(SOFTMAX, x, ids, w.view(4, 2), w.view(4, 2)),
+                 lambda: mxg.mx_moe_permute(y, a, y), lambda: mxg.mx_moe_permute_backward(y, a, y),
+                 lambda: mxg.mx_moe_combine_backward(y, d, a, w, d, w.clone()),
+                 lambda: mxg.mx_moe_combine_backward(y, d, a, w, torch.empty_like(d), w)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+
+
 def test_repeated_rows_are_refused_under_validation(monkeypatch):
     x = torch.zeros((2, 8), dtype=torch.bfloat16, device="cuda")
     rows = torch.zeros((4, 8), dtype=torch.bfloat16, device="cuda")
