@@ -104,6 +104,19 @@ __device__ __forceinline__ void lds_dma16_rows(const void* base_in, const uint32
             : "memory", "m0", "scc");
 }
 
+// The lane number.  FRESH: made anew where it is needed, so that what derives from
+// it (loader rows, fragment addresses) holds no register between stages: for a wave
+// of 128 accumulators, 225 registers instead of 256 (65536 uneven rows 516 -> 500 us,
+// 8192^3 490 -> 480).  Smaller tiles have registers to spare and keep it (made anew,
+// 128-row tiles 122 -> 126 us on 8192 rows of 32 groups, 32-row tiles 22.2 -> 24.4).
+template <bool FRESH>
+__device__ __forceinline__ int lane_id() {
+    if constexpr (!FRESH) return threadIdx.x & (kWave - 1);
+    int l;
+    __asm__ volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+    return l;
+}
+
 __device__ __forceinline__ v4f mma128(const v8i& n, const v8i& t) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, t, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
@@ -128,10 +141,10 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     __shared__ int32_t s_ids[kTables ? kMaxGroups : 1];
     __shared__ uint32_t s_wave[NW];
 
-    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    constexpr bool kFresh = TM * TN * 4 >= 128;
+    const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wm = wave / TL::WGN, wn = wave % TL::WGN;
-    const int l16 = lane & 15, kg = lane >> 4;
     const int G = args.G;
 
     if constexpr (kTables)
@@ -158,6 +171,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         const int64_t L = split ? ws.full + (W - ws.full) / 2 : W;
         const int64_t ntn = args.ntiles_n;
         const uint32_t x = (uint32_t)(L / ntn);  // M tile of the launch
+        const int lane = lane_id<kFresh>(), l16 = lane & 15;
         uint64_t m = __ballot(lane * 16 <= G && s_pre[lane * 16 <= G ? lane * 16 : 0] <= x);
         const int base = (__popcll(m) - 1) * 16;
         const int idx = base + l16;
@@ -202,12 +216,13 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     int pk = 0;          // its next stage
     int pslot = 0;       // ring slot that stage goes to
     int pchunk = 0;      // scale buffer of its chunk
-    const int r0 = wave * 8 + lane / 8;               // row of this lane in load 0 (+ 8 NW per load)
-    const int chunk = swz_chunk<kSB>(r0, lane % 8);   // 16-byte piece it fetches: the swizzle
     const int ring0 = (int)lds_addr(s_ring), scl0 = (int)lds_addr(s_scl);
     uint32_t a_off[A_J], b_off[B_J];
     const uint8_t *p_a = nullptr, *p_b = nullptr;  // the tile's operands at the producer's stage
     auto set_tile = [&]() {
+        const int lane = lane_id<kFresh>();
+        const int r0 = wave * 8 + lane / 8;              // row of this lane in load 0 (+ 8 NW per load)
+        const int chunk = swz_chunk<kSB>(r0, lane % 8);  // 16-byte piece it fetches: the swizzle
         p_a = args.a + pc.m0 * K;
         p_b = args.b + ((int64_t)pc.e * args.N + pc.n0) * K;
         // rows past the group and columns past N re-read the last real one
@@ -228,6 +243,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         if (pk == 0) set_tile();
         if (pk == nkt - 1 && K % kSB != 0) {
             // pieces past the end of K fetch the stage's first one instead; the consumer zeroes them
+            const int lane = lane_id<kFresh>(), chunk = swz_chunk<kSB>(wave * 8 + lane / 8, lane % 8);
             const uint32_t back = (int64_t)pk * kSB + chunk * 16 < K ? 0 : chunk * 16;
 #pragma unroll
             for (int j = 0; j < A_J; ++j) a_off[j] -= back;
@@ -245,7 +261,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
             pchunk = pchunk + 1 < kSlots ? pchunk + 1 : 0;
             const int dst = scl0 + pchunk * kScl;
             // kSclBlocks blocks of each of 64 / kSclBlocks rows per load; blocks past the last re-read it
-            const int blk = pk + lane % kSclBlocks;
+            const int lane = lane_id<kFresh>(), blk = pk + lane % kSclBlocks;
             const uint32_t col = (uint32_t)(blk < nkt ? blk : nkt - 1);
             const float* as = static_cast<const float*>(args.as) + pc.m0 * nkt;
 #pragma unroll
@@ -285,15 +301,13 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     // Waves w and w + 4 share a SIMD.  The upper half issues its loads of a stage
     // behind its first products instead of before its fragment reads, so that one
     // wave of a SIMD multiplies while the other issues loads and waits for its
-    // fragments (256-row tiles 520 -> 507 us on 65536 uneven rows, 128-row tiles
-    // 28.7 -> 27.1 us on 5003; behind the 8th product 532, all waves so 554).
+    // fragments (3 % less time for the 256-row tiles on 65536 uneven rows, 6 % for
+    // the 128-row tiles on 5003; behind the 8th product 2 % more, all waves so 6 %
+    // more; reading the next stage's fragments behind the last products: no gain).
     constexpr int kLate = 3;
     const bool late = NW == 8 && wave >= NW / 2;
     stage_barrier<0>();
     int cslot = 0, cchunk = 0;
-    // fragment addresses inside a slot: row l16 of the wave's first 16, pieces kg and kg + 4
-    const int fa = (wm * WTM + l16) * kSB, fb = kAStage + (wn * WTN + l16) * kSB;
-    const int p0 = swz_chunk<kSB>(l16, kg) << 4, p1 = p0 ^ 64;
     bool drain = false;  // stores of an epilogue are outstanding: counted waits do not hold
 
     while (cw < ws.items) {
@@ -312,7 +326,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
                 // the pieces past the end of K hold other bytes: zero them
                 const int good = (int)(K % kSB) / 16;
                 uint8_t* z = s_ring + cslot * kStage;
-                for (int r = tid; r < BM + BN; r += NT) {
+                for (int r = wave * kWave + lane_id<kFresh>(); r < BM + BN; r += NT) {
                     const int row = r < BM ? r : r - BM;
                     for (int p = good; p < 8; ++p)
                         *reinterpret_cast<uint4*>(z + (r < BM ? 0 : kAStage) + swz<kSB>(row, p)) =
@@ -324,6 +338,10 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
                 __asm__ volatile("" ::: "memory");
             }
             if (wave_live) {
+                // fragment addresses inside the slot: row l16 of the wave's first 16, pieces kg and kg + 4
+                const int lane = lane_id<kFresh>(), l16 = lane & 15;
+                const int fa = (wm * WTM + l16) * kSB, fb = kAStage + (wn * WTN + l16) * kSB;
+                const int p0 = swz_chunk<kSB>(l16, lane >> 4) << 4, p1 = p0 ^ 64;
                 auto frag = [&](int at) {
                     const uint4 x0 = *reinterpret_cast<const uint4*>(cur + at + p0);
                     const uint4 x1 = *reinterpret_cast<const uint4*>(cur + at + p1);
@@ -377,6 +395,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         // at a time, 16-byte pieces XOR-swizzled by the row so that the lanes'
         // 8-byte writes (16 rows at one column) and the readers' whole rows are
         // both conflict-free, then written out in 16-byte pieces.
+        const int lane = lane_id<kFresh>(), l16 = lane & 15, kg = lane >> 4, tid = wave * kWave + lane;
         uint8_t* stg = s_ring + cslot * kStage;
         if ((args.N & 7) == 0) {
             constexpr int kPasses = BM * BN * 2 > kStage ? 2 : 1;
@@ -449,10 +468,11 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
 // A lane's operand pieces are 64 bytes apart (pieces kg and kg + 4 of a block),
 // so the four lanes of a row read 64 bytes together; with the nontemporal hint
 // the two halves of a line were fetched twice (K 7168, N 2048, 8 rows of 64
-// experts: 27.5 us against 22.2).  Measured there, 8 rows: 22.2 us (5.3 TB/s of
-// weights; the 32 x 128 tile 38.6); 64 rows: 107 us (120); one 16-column
-// fragment a wave instead of two 108, eight waves instead of four 163, eight
-// blocks ahead instead of four 132, two row blocks of 16 instead of one 134.
+// experts: a quarter more time).  Measured there, 8 rows: 25 us (4.6 TB/s of
+// weights; the 32 x 128 tile 36); 64 rows, a few a group: 105 us (120), and on the
+// same rows one 16-column fragment a wave instead of two 1 % more, eight waves
+// instead of four 50 %, eight blocks ahead instead of four 23 %, two row blocks of
+// 16 instead of one 25 %.
 template <int NF, int SPLIT>
 __global__ __launch_bounds__(SPLIT * kWave, 1) void block128_rows_kernel(const GemmArgs args) {
     constexpr int kDeep = 4, kCols = NF * 16, kRows = 16, NT = SPLIT * kWave;
@@ -489,7 +509,8 @@ __global__ __launch_bounds__(SPLIT * kWave, 1) void block128_rows_kernel(const G
                 const int64_t at = (int64_t)kb * kSB + (kg + 4 * c) * 16;
                 const bool in = !tail || at < K;
 #pragma unroll
-                for (int f = 0; f < NF; ++f) wb[d][f][c] = in ? *reinterpret_cast<const uint4*>(bp[f] + at) : make_uint4(0, 0, 0, 0);
+                for (int f = 0; f < NF; ++f)
+                    wb[d][f][c] = in ? *reinterpret_cast<const uint4*>(bp[f] + at) : make_uint4(0, 0, 0, 0);
                 ta[d][c] = in ? *reinterpret_cast<const uint4*>(ap + at) : make_uint4(0, 0, 0, 0);
             }
             sa[d] = sp[kb];
@@ -599,15 +620,16 @@ hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream
         return (mt * ((p.N + BN - 1) / BN) + cus - 1) / cus;
     };
     // A round of 256 x 256 tiles takes 66 us at K = 4096, of 128 x 256 tiles 44,
-    // of 32 x 128 tiles 20 to 25; the fewest weighted rounds win.  Measured (us, 256 / 128 / 32 rows a tile):
-    // 65536 rows of 128 uneven experts, 4096 x 1536: 520 / 595 / 2010; 5003 of
-    // 24, 2080 x 1000: 42 / 30 / 76; 4096 of 64, 4096 x 2048: 142 / 133 / 214;
-    // 256 of 4, 4096 x 2048: - / 41 / 25; 400 of 2: - / 42 / 24.
+    // of 32 x 128 tiles 20 to 25; the fewest weighted rounds win.  Measured on
+    // operands that no cache holds (us, 256 / 128 / 32 rows a tile): 65536 rows of
+    // 128 uneven experts, 4096 x 1536: 500 / 602 / 1826; 5003 of 24, 2080 x 1000:
+    // 51 / 34 / 73; 4096 of 64, 4096 x 2048: 153 / 138 / 197; 256 of 4, 4096 x
+    // 2048: - / 38 / 23; 400 of 2: - / 38 / 23.
     const int64_t c256 = 66 * rounds(256, 256), c128 = 44 * rounds(128, 256), c32 = 24 * rounds(32, 128);
-    // The row kernel reads an expert's weights once per 16 rows: 4 rows a group
-    // 154 us against 160 for the tiles, 8 rows 174 against 162 (64 experts, 7168
-    // x 2048); where the 32 x 128 tiles do not fill the chip it still wins at 8
-    // rows (8 experts, 2048 x 1024: 12.4 us against 15.4).
+    // The row kernel reads an expert's weights once per 16 rows: 2 rows a group
+    // 133 us against 147 for the tiles, 4 rows 159 against 164, 8 rows 177 against
+    // 168 (64 experts, 7168 x 2048); where the 32 x 128 tiles do not fill the chip
+    // it still wins at 8 rows (8 experts, 2048 x 1024: 10.6 us against 14.5).
     const bool wide_grid = (p.N + kRowCols - 1) / kRowCols * p.G < (1 << 22);
     if (wide_grid && (rows <= 4 || (rows <= 16 && (p.N + 127) / 128 * groups < cus))) return launch_rows(p, stream);
     if (c32 < c128 && c32 < c256) return launch_tile<TileSmall>(p, stream, 1 << 30);

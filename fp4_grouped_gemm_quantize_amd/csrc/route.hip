@@ -6,7 +6,8 @@
 //
 // All three are small integer or scalar jobs over [tokens, experts] or [slots]
 // arrays, bound by latency: each is one launch, without workspace or atomics,
-// so results do not depend on timing.
+// so results do not depend on timing.  Measured (time on the device): choice of 8
+// from 128 experts for 8192 tokens 6.3 us, its gradient 4.5, 64 tokens 6.1.
 #include <type_traits>
 
 #include "mxg_device.h"
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void topk_backward_kernel(const LT* __res
                 d = scale * dweights[t * top_k + sub];
             }
         }
-        if (mine == -INFINITY) id = -1;  // its weight is 0 whatever the logit's neighbourhood
+        if (mine == -INFINITY) id = -1;  // a score of 0: its weight is 0 and stays so
         const bool live = id >= 0;
 
         float g = 0.0f, top = 0.0f, total = 1.0f, x[VPL];
@@ -289,8 +290,9 @@ __global__ __launch_bounds__(kThreads) void topk_backward_kernel(const LT* __res
 // when one expert takes most slots.  Bound by instruction issue (a compare for
 // each of the two questions, the counts on the scalar unit).  Up to 8 steps a
 // wave (n <= 65536) the matches are kept as eight bits a step, past that the
-// second pass reads the ids again.  Measured, 65536 slots of 128 experts: 21 us
-// with one id a lane and step, 13 with four and a ballot for each.
+// second pass reads the ids again.  Measured, 65536 slots of 128 experts: 8.2 us (21
+// with one id a lane and step, 13 with four and a ballot for each, 26 with the
+// slots of an expert split over workgroups); 1024 slots of 64: 3.2 us.
 constexpr int kKeep = 8, kIds = 8;
 
 // Eight consecutive ids, -1 past the end.  inside (wave-uniform): all are before
