@@ -1,6 +1,6 @@
 // api_moe.cpp -- the extern "C" entry points of the router, the routing plan,
 // the 128-block FP8 format and their gradients: argument validation on the
-// host (before anything is enqueued), then one launch per call.  No
+// host (before anything is enqueued), then one launch (a long sort: four).  No
 // allocation outside the MXG_VALIDATE check, no host synchronisation outside
 // it, no state.  No exception leaves an entry point.
 #include "api_common.h"

@@ -5,8 +5,8 @@
 //  these arrays and do not say how they are made.)
 //
 // All three are small integer or scalar jobs over [tokens, experts] or [slots]
-// arrays, bound by latency: each is one launch, without workspace or atomics,
-// so results do not depend on timing.  Measured (time on the device): choice of 8
+// arrays, bound by latency: each is one launch (the sort of very many slots four),
+// without workspace, and results do not depend on timing.  Measured (time on the device): choice of 8
 // from 128 experts for 8192 tokens 6.3 us, its gradient 4.5, 64 tokens 5.9.
 #include <type_traits>
 
@@ -284,7 +284,8 @@ __global__ __launch_bounds__(kThreads) void topk_backward_kernel(const LT* __res
 }
 
 // ---------------------------------------------------------------------------
-// Stable counting sort of n slots by expert id, one workgroup per expert.
+// Stable counting sort of n slots by expert id, one workgroup per expert (very many
+// slots: see sort_count_kernel).
 // Workgroup e reads every id (the whole list is a few hundred KB at most and
 // stays in L2): the ids below e give its first row, the ids equal to e, in slot
 // order, its rows.  A wave owns a contiguous stretch of the slots and takes 512
@@ -293,9 +294,9 @@ __global__ __launch_bounds__(kThreads) void topk_backward_kernel(const LT* __res
 // counts) and of its own lane's ids before.  Reading the list once per expert
 // needs neither a workspace nor a second launch, nor atomics whose speed falls
 // when one expert takes most slots.  Bound by instruction issue (a compare for
-// each of the two questions, the counts on the scalar unit).  Up to 8 steps a
-// wave (n <= 65536) the matches are kept as eight bits a step, past that the
-// second pass reads the ids again.  Measured, 65536 slots of 128 experts: 8.2 us (21
+// each of the two questions, the counts on the scalar unit).  The matches are kept
+// as eight bits a step, of 8 steps a wave at most (65536 slots; longer lists go to
+// the kernels below).  Measured, 65536 slots of 128 experts: 8.2 us (21
 // with one id a lane and step, 13 with four and a ballot for each, 26 with the
 // slots of an expert split over workgroups); 1024 slots of 64: 3.2 us.
 constexpr int kKeep = 8, kIds = 8;
@@ -359,31 +360,26 @@ __global__ __launch_bounds__(NT) void sort_kernel(const int32_t* __restrict__ id
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t e = blockIdx.x;
     constexpr int kStep = kIds * kWave;
-    const int64_t steps = (n + (int64_t)NW * kStep - 1) / ((int64_t)NW * kStep);  // per wave
-    const int64_t base = wave * steps * kStep + lane * kIds;  // this lane's first slot
-    const bool inside = (wave + 1) * steps * kStep <= n;
+    const int steps = (int)((n + NW * kStep - 1) / (NW * kStep));  // per wave, at most kKeep
+    const int64_t base = (int64_t)wave * steps * kStep + lane * kIds;  // this lane's first slot
+    const bool inside = (int64_t)(wave + 1) * steps * kStep <= n;
 
     uint32_t less = 0, same = 0, hits[kKeep / 4] = {};  // hits: eight bits a step
-    if (steps <= kKeep) {
-        Ids v[kKeep];
-        if (inside) {
-#pragma unroll
-            for (int s = 0; s < kKeep; ++s)
-                if (s < steps) v[s] = load_ids(ids, base + (int64_t)s * kStep, n, true);
-        } else {
-#pragma unroll
-            for (int s = 0; s < kKeep; ++s)
-                if (s < steps) v[s] = load_ids(ids, base + (int64_t)s * kStep, n, false);
-        }
+    Ids v[kKeep];
+    if (inside) {
 #pragma unroll
         for (int s = 0; s < kKeep; ++s)
-            if (s < steps) hits[s / 4] |= match(v[s], e, less) << (8 * (s % 4));
-#pragma unroll
-        for (int h = 0; h < kKeep / 4; ++h) same += __popc(hits[h]);
+            if (s < steps) v[s] = load_ids(ids, base + (int64_t)s * kStep, n, true);
     } else {
-#pragma unroll 4
-        for (int64_t s = 0; s < steps; ++s) same += __popc(match(load_ids(ids, base + s * kStep, n, inside), e, less));
+#pragma unroll
+        for (int s = 0; s < kKeep; ++s)
+            if (s < steps) v[s] = load_ids(ids, base + (int64_t)s * kStep, n, false);
     }
+#pragma unroll
+    for (int s = 0; s < kKeep; ++s)
+        if (s < steps) hits[s / 4] |= match(v[s], e, less) << (8 * (s % 4));
+#pragma unroll
+    for (int h = 0; h < kKeep / 4; ++h) same += __popc(hits[h]);
     same = (uint32_t)__builtin_amdgcn_readlane((int)lane_scan(same), kWave - 1);
     if (lane == 0) {
         s_less[wave] = less;
@@ -417,17 +413,9 @@ __global__ __launch_bounds__(NT) void sort_kernel(const int32_t* __restrict__ id
         run += (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
     };
     if (same) {  // wave-uniform
-        if (steps <= kKeep) {
 #pragma unroll
-            for (int s = 0; s < kKeep; ++s)
-                if (s < steps) place(base + (int64_t)s * kStep, (hits[s / 4] >> (8 * (s % 4))) & 255u);
-        } else {
-            for (int64_t s = 0; s < steps; ++s) {
-                uint32_t unused = 0;
-                const int64_t i = base + s * kStep;
-                place(i, match(load_ids(ids, i, n, inside), e, unused));
-            }
-        }
+        for (int s = 0; s < kKeep; ++s)
+            if (s < steps) place(base + (int64_t)s * kStep, (hits[s / 4] >> (8 * (s % 4))) & 255u);
     }
     // the last expert's workgroup, which knows the total: dropped slots and the rows past the last
     if ((int)e == E - 1 && (int64_t)total < n) {
@@ -436,6 +424,130 @@ __global__ __launch_bounds__(NT) void sort_kernel(const int32_t* __restrict__ id
             if (i >= (int64_t)total) slot_of_row[i] = -1;
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// The same sort for many slots, where reading the list once per expert costs more
+// than four launches: the list is cut into chunks of kChunkSlots (the last takes the
+// rest), each workgroup counts its chunk's slots per expert, the counts are summed
+// over the chunks and the experts, and each workgroup places its chunk.  The counts
+// need no workspace: chunk c's lie in the first E entries of its own stretch of
+// row_of_slot (E <= MXG_MAX_GROUPS <= kChunkSlots), which only the workgroup that
+// reads them overwrites, in the last launch.  Bound by the launches up to 1 M slots
+// (23 us a call), past that by the scattered stores of the place kernel.
+constexpr int kChunkSlots = 4096, kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
+static_assert(kMaxGroups <= kChunkSlots && kMaxGroups <= kSortThreads, "a chunk holds its counts, a thread an expert");
+
+// Counts of chunk c: LDS atomics, integers, so their order changes nothing.
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                                  int32_t* __restrict__ table) {
+    __shared__ uint32_t s_count[kMaxGroups];
+    for (int e = threadIdx.x; e < E; e += kSortThreads) s_count[e] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)blockIdx.x * kChunkSlots;
+    const int64_t hi = blockIdx.x + 1 < gridDim.x ? lo + kChunkSlots : n;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+        const uint32_t id = (uint32_t)ids[i];
+        if (id < (uint32_t)E) atomicAdd(&s_count[id], 1u);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kSortThreads) table[lo + e] = (int32_t)s_count[e];
+}
+
+// Running sums of an expert's counts over the chunks; its total to off[e].
+// 16 experts a workgroup, 16 threads share an expert's chunks.
+__global__ __launch_bounds__(kThreads) void sort_scan_kernel(int32_t* __restrict__ table, int64_t chunks, int E,
+                                                             uint32_t* __restrict__ off) {
+    __shared__ uint32_t s_sum[16][16];
+    const int le = threadIdx.x % 16, seg = threadIdx.x / 16, e = blockIdx.x * 16 + le;
+    const int64_t per = (chunks + 15) / 16, lo = seg * per, hi = lo + per < chunks ? lo + per : chunks;
+    uint32_t sum = 0;
+    if (e < E)
+        for (int64_t c = lo; c < hi; ++c) sum += (uint32_t)table[c * kChunkSlots + e];
+    s_sum[seg][le] = sum;
+    __syncthreads();
+    uint32_t run = 0, total = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        run += q < seg ? s_sum[q][le] : 0;
+        total += s_sum[q][le];
+    }
+    if (e >= E) return;
+    for (int64_t c = lo; c < hi; ++c) {
+        const uint32_t t = (uint32_t)table[c * kChunkSlots + e];
+        table[c * kChunkSlots + e] = (int32_t)run;
+        run += t;
+    }
+    if (seg == 0) off[e] = total;
+}
+
+// The experts' totals to their offsets, in place: one workgroup.
+__global__ __launch_bounds__(kSortThreads) void sort_offsets_kernel(uint32_t* __restrict__ off, int E) {
+    __shared__ uint32_t s_wave[kSortWaves];
+    const int e = threadIdx.x, lane = e & (kWave - 1), wave = e / kWave;
+    const uint32_t mine = e < E ? off[e] : 0, upto = lane_scan(mine);
+    if (lane == kWave - 1) s_wave[wave] = upto;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < wave; ++w) before += s_wave[w];
+    if (e < E) off[e] = before + upto - mine;
+    if (e == E - 1) off[E] = before + upto;
+}
+
+// The lanes of the wave whose id equals this one's, of the lanes that hold one.
+__device__ __forceinline__ uint64_t same_id(uint32_t id, bool has, int bits) {
+    uint64_t m = __ballot(has);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (id >> b) & 1;
+        const uint64_t with = __ballot(one);
+        m &= one ? with : ~with;
+    }
+    return m;
+}
+
+// Places chunk c.  A wave owns a contiguous stretch of it and takes 64 slots a step;
+// a slot's row is its expert's offset, plus the expert's slots in the chunks and waves
+// and steps before, plus the lanes before it with the same id.
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                                  int bits, const uint32_t* __restrict__ off,
+                                                                  int32_t* row_of_slot,
+                                                                  int32_t* __restrict__ slot_of_row) {
+    __shared__ uint32_t s_next[kSortWaves][kMaxGroups];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t lo = (int64_t)blockIdx.x * kChunkSlots;
+    const int64_t hi = blockIdx.x + 1 < gridDim.x ? lo + kChunkSlots : n;
+    for (int e = lane; e < E; e += kWave) s_next[wave][e] = 0;
+    const int64_t per = ((hi - lo + kSortWaves - 1) / kSortWaves + kWave - 1) / kWave * kWave;
+    const int64_t w_lo = lo + wave * per, w_hi = w_lo + per < hi ? w_lo + per : hi;
+    const uint64_t below = (1ull << lane) - 1;
+    auto step = [&](int64_t i0, auto use) {
+        const uint32_t id = i0 + lane < w_hi ? (uint32_t)ids[i0 + lane] : ~0u;
+        const bool has = id < (uint32_t)E;
+        const uint64_t m = same_id(id, has, bits);
+        const uint32_t next = has ? s_next[wave][id] : 0;
+        use(i0 + lane, has, next + (uint32_t)__popcll(m & below));
+        if (has && (m & below) == 0) s_next[wave][id] = next + (uint32_t)__popcll(m);  // the first lane of each id
+    };
+    for (int64_t i = w_lo; i < w_hi; i += kWave) step(i, [](int64_t, bool, uint32_t) {});
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kSortThreads) {
+        uint32_t run = off[e] + (uint32_t)row_of_slot[lo + e];
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t t = s_next[w][e];
+            s_next[w][e] = run;
+            run += t;
+        }
+    }
+    __syncthreads();  // the chunk's counts are read: its stretch of row_of_slot may be written
+    for (int64_t i = w_lo; i < w_hi; i += kWave)
+        step(i, [&](int64_t slot, bool has, uint32_t row) {
+            if (slot < w_hi) row_of_slot[slot] = has ? (int32_t)row : -1;
+            if (has) slot_of_row[row] = (int32_t)slot;
+        });
+    const int64_t total = off[E];
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
+        if (i >= total) slot_of_row[i] = -1;
 }
 
 // A launch holds fewer than 2^32 threads; past this many workgroups they loop.
@@ -516,6 +628,26 @@ hipError_t launch_topk_backward(int type, int score, const void* logits, const i
 
 hipError_t launch_sort(const int32_t* ids, int64_t nslots, int E, uint32_t* off, int32_t* row_of_slot,
                        int32_t* slot_of_row, hipStream_t stream) {
+    // The one launch reads the list once per expert, two workgroups on a CU: it wins up
+    // to 65536 slots of 256 experts (8.6 us a call against 17), draws at twice that (16
+    // and 16) and loses where more of either follows (16384 slots of 1024: 14 and 17,
+    // 65536: 26 and 17; 1 M slots of 128: 125 and 23, of 1024: 447 and 29; 4 M of 256:
+    // 490 and 66; with 97 % of 1 M slots on one expert 822 and 24).
+    constexpr int64_t kOnceSlots = 65536;
+    static_assert(kOnceSlots <= kKeep * 1024 * kIds, "the matches a wave keeps");
+    if (nslots * (E > 256 ? E : 256) > kOnceSlots * 256) {
+        const int64_t chunks = nslots / kChunkSlots;
+        int bits = 0;
+        while ((1 << bits) < E) ++bits;
+        hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)chunks), dim3(kSortThreads), 0, stream, ids, nslots, E,
+                           row_of_slot);
+        hipLaunchKernelGGL(sort_scan_kernel, dim3((unsigned)((E + 15) / 16)), dim3(kThreads), 0, stream, row_of_slot,
+                           chunks, E, off);
+        hipLaunchKernelGGL(sort_offsets_kernel, dim3(1), dim3(kSortThreads), 0, stream, off, E);
+        hipLaunchKernelGGL(sort_place_kernel, dim3((unsigned)chunks), dim3(kSortThreads), 0, stream, ids, nslots, E,
+                           bits, off, row_of_slot, slot_of_row);
+        return hipGetLastError();
+    }
     // four waves are enough for a serving step's slots and start sooner
     if (nslots <= 4096)
         hipLaunchKernelGGL(sort_kernel<256>, dim3((unsigned)E), dim3(256), 0, stream, ids, nslots, E, off, row_of_slot,

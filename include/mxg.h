@@ -651,7 +651,7 @@ mxg_status mx_moe_topk_backward(mxg_dtype logits_type, mxg_score score, const vo
  *   slot_of_row  int32 [num_tokens * top_k]: the slot of each routed row, -1 past
  *                the last (mx_grouped_quantize_gather, with indices_divisor =
  *                top_k).
- * Rows are in the order (expert, slot): deterministic, no atomics.  The outputs
+ * Rows are in the order (expert, slot): deterministic.  The outputs
  * may not overlap topk_ids (every workgroup reads all of it) or each other.
  *
  * Errors: INVALID_VALUE for num_tokens < 0, top_k < 1, num_experts < 1, a null

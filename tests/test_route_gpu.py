@@ -266,6 +266,60 @@ def test_sort(S, k, E, law):
         assert np.array_equal(g.numpy(), want)
 
 
+@pytest.mark.parametrize("S,k,E", [(8193, 8, 256), (16411, 8, 128), (2063, 8, 1024), (70001, 1, 1), (70001, 1, 3),
+                                   (140000, 1, 1000), (17000, 64, 64)])
+@pytest.mark.parametrize("law", ["even", "one", "dropped", "none"])
+def test_sort_of_many(S, k, E, law):
+    """Lists that are cut into chunks: a last chunk longer than the others, counts of up to
+    1024 experts, one expert or none with (nearly) all slots."""
+    rng = np.random.default_rng(S + E)
+    ids = rng.integers(0, E, (S, k)).astype(np.int32)
+    if law == "one":
+        ids[rng.random((S, k)) < 0.97] = E // 2
+    elif law == "dropped":
+        ids[rng.random((S, k)) < 0.3] = -1
+        ids[rng.random((S, k)) < 0.1] = E
+    elif law == "none":
+        ids[:] = -5
+    g = [Guarded(np.full(n, 7, np.int32)) for n in (E + 1, S * k, S * k)]
+    mxg.mx_moe_sort(to_gpu(ids), *(x.view() for x in g))
+    torch.cuda.synchronize()
+    for got, want in zip(g, ref_sort(ids, E)):
+        got.check()
+        assert np.array_equal(got.numpy(), want)
+
+
+def test_sort_of_many_in_a_graph_and_on_two_streams():
+    """Replays with other ids, and two such sorts at once, give what the calls alone give."""
+    S, k, E = 16411, 8, 200
+    rng = np.random.default_rng(0)
+    lists = [rng.integers(-1, E + 1, (S, k)).astype(np.int32) for _ in range(3)]
+    want = [ref_sort(v, E) for v in lists]
+    ids = to_gpu(lists[0])
+    out = mxg.moe_sort(ids, E)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mxg.mx_moe_sort(ids, *out)
+    for i in (1, 2, 0, 1):
+        ids.copy_(to_gpu(lists[i]))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip(out, want[i]):
+            assert np.array_equal(got.cpu().numpy(), w)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    gpu = [to_gpu(v) for v in lists]
+    torch.cuda.synchronize()
+    res = []
+    for rep in range(4):
+        for s, v in zip(streams, gpu):
+            with torch.cuda.stream(s):
+                res.append(mxg.moe_sort(v, E))
+    torch.cuda.synchronize()
+    for i, r in enumerate(res):
+        for got, w in zip(r, want[i % 2]):
+            assert np.array_equal(got.cpu().numpy(), w)
+
+
 def test_sort_without_tokens():
     off = torch.full((6,), 9, dtype=torch.int32, device="cuda")
     none = torch.empty((0,), dtype=torch.int32, device="cuda")
@@ -382,7 +436,8 @@ def test_outputs_over_inputs_are_refused():
     y, d = torch.zeros((2, 4, 8), dtype=torch.bfloat16, device="cuda")
     w = torch.zeros(8, device="cuda")
     for call in (lambda: mxg.mx_moe_sort(ids, off, ids.view(-1), b), lambda: mxg.mx_moe_sort(ids, off, a, ids.view(-1)),
-                 lambda: mxg.mx_moe_sort(ids, off, a, a), lambda: mxg.mx_moe_topk_backward(SOFTMAX, x, ids, w.view(4, 2), x),
+                 lambda: mxg.mx_moe_sort(ids, off, a, a),
+                 lambda: mxg.mx_moe_topk_backward(SOFTMAX, x, ids, w.view(4, 2), x),
                  lambda: mxg.mx_moe_topk_backward(SOFTMAX, x, ids, w.view(4, 2), w.view(4, 2)),
                  lambda: mxg.mx_moe_permute(y, a, y), lambda: mxg.mx_moe_permute_backward(y, a, y),
                  lambda: mxg.mx_moe_combine_backward(y, d, a, w, d, w.clone()),
