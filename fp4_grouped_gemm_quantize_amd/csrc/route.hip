@@ -7,7 +7,8 @@
 // All three are small integer or scalar jobs over [tokens, experts] or [slots]
 // arrays, bound by latency: each is one launch (the sort of very many slots four),
 // without workspace, and results do not depend on timing.  Measured (time on the device): choice of 8
-// from 128 experts for 8192 tokens 6.3 us, its gradient 4.5, 64 tokens 5.9.
+// from 128 experts for 8192 tokens and its gradient 7.7 us, choice of 8 from 64
+// under a bias for 64 tokens 4.3.
 #include <type_traits>
 
 #include "mxg_device.h"
@@ -26,10 +27,10 @@ constexpr int kThreads = 256;
 // equal inside each quad / half.  Wider groups add shuffles over 16 and 32.
 template <int STEP>
 __device__ __forceinline__ uint32_t exchange(uint32_t v) {
-    if constexpr (STEP == 0) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xf, 0xf, false);
-    else if constexpr (STEP == 1) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xf, 0xf, false);
-    else if constexpr (STEP == 2) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xf, 0xf, false);
-    else if constexpr (STEP == 3) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xf, 0xf, false);
+    if constexpr (STEP == 0) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);
+    else if constexpr (STEP == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);
+    else if constexpr (STEP == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);
+    else if constexpr (STEP == 3) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true);
     else return (uint32_t)__shfl_xor((int)v, 1 << STEP, kWave);
 }
 template <int STEP>
@@ -79,10 +80,10 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
     return v > -INFINITY ? ((u >> 31) ? ~u : u | 0x80000000u) : 0u;
 }
-__device__ __forceinline__ uint64_t order_key(double v) {
-    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
-    return v > -(double)INFINITY ? ((u >> 63) ? ~u : u | 0x8000000000000000ull) : 0ull;
-}
+// Biased scores are compared as they are, -infinity for what may not be chosen.
+__device__ __forceinline__ double order_key(double v) { return v > -(double)INFINITY ? v : -(double)INFINITY; }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 // log(1 / (1 + e^-x)), exact where the sigmoid itself underflows
@@ -91,10 +92,12 @@ __device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.0f) - 
 // ---------------------------------------------------------------------------
 // LPT lanes hold a token's logits, expert i in lane i % LPT (element i / LPT),
 // so loads are coalesced and a lane's elements rise with their index.  Each of
-// the top_k rounds takes the largest key of the lane's own elements, then of
-// the token's lanes (equal keys: the lower index), and clears the winner's.
-// 16 lanes a token hold four tokens a wave: a round is then VPL compares and
-// four register exchanges for all four.  Lane j ends with slot j, so 16 lanes
+// the top_k rounds takes the largest key over the lane's own elements and the
+// token's lanes, then the lowest index that has it, and clears that one: maxima
+// and minima alone, which the exchanges' register moves fold into (carrying each
+// key's index through the maximum: 65536 x 128, 8 of them, 20.8 us instead of
+// 16.1; 8192 x 128, 32 of them, 35 instead of 21).  16 lanes a token hold four
+// tokens a wave, so a round serves four.  Lane j ends with slot j, so 16 lanes
 // serve top_k <= 16.
 template <class LT, int LPT, int VPL, bool BIASED>
 __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ logits, const float* __restrict__ bias,
@@ -104,7 +107,8 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ l
     const int sub = threadIdx.x % LPT;
     for (int64_t t0 = (int64_t)blockIdx.x * (kThreads / LPT); t0 < ntok; t0 += (int64_t)gridDim.x * (kThreads / LPT)) {
         const int64_t t = t0 + threadIdx.x / LPT;
-        using Key = typename std::conditional<BIASED, uint64_t, uint32_t>::type;
+        using Key = typename std::conditional<BIASED, double, uint32_t>::type;
+        const Key none = BIASED ? (Key)-INFINITY : (Key)0;
         const bool on = t < ntok;  // the lanes of a token past the end stay for the exchanges
         const LT* row = logits + (on ? t : 0) * E;
 
@@ -114,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ l
             const int i = v * LPT + sub;
             x[v] = on && i < E ? load_logit(row + i) : -INFINITY;
         }
-        float b[BIASED ? VPL : 1];  // loaded beside the logits, not behind the scores (64 tokens: 6.4 -> 5.9 us)
+        float b[BIASED ? VPL : 1];  // loaded beside the logits, not behind the scores (64 tokens: 0.5 us less)
         if constexpr (BIASED) {
 #pragma unroll
             for (int v = 0; v < VPL; ++v) b[v] = bias[v * LPT + sub < E ? v * LPT + sub : 0];
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ l
 #pragma unroll
             for (int v = 0; v < VPL; ++v) {
                 const int i = v * LPT + sub;
-                key[v] = 0;
+                key[v] = none;
                 if (i < E && x[v] > -INFINITY) {
                     const double s = score == 0 ? exp((double)x[v] - (double)top) / total
                                                 : 1.0 / (1.0 + exp(-(double)x[v]));
@@ -152,30 +156,17 @@ __global__ __launch_bounds__(kThreads) void topk_kernel(const LT* __restrict__ l
         int32_t my_id = -1;
         for (int k = 0; k < top_k; ++k) {
             Key best = key[0];
-            uint32_t at = (uint32_t)sub;
 #pragma unroll
-            for (int v = 1; v < VPL; ++v)
-                if (key[v] > best) {
-                    best = key[v];
-                    at = (uint32_t)(v * LPT + sub);
-                }
-            auto step = [&](Key ok, uint32_t oi) {
-                const bool take = ok > best || (ok == best && oi < at);
-                best = take ? ok : best;
-                at = take ? oi : at;
-            };
-            step(exchange<0>(best), exchange<0>(at));
-            step(exchange<1>(best), exchange<1>(at));
-            step(exchange<2>(best), exchange<2>(at));
-            step(exchange<3>(best), exchange<3>(at));
-            if constexpr (LPT == 64) {
-                step(exchange<4>(best), exchange<4>(at));
-                step(exchange<5>(best), exchange<5>(at));
-            }
-            if (sub == k) my_id = best ? (int32_t)at : -1;
+            for (int v = 1; v < VPL; ++v) best = larger(best, key[v]);
+            best = reduce<LPT>(best, [](Key p, Key q) { return larger(p, q); });
+            uint32_t at = ~0u;
+#pragma unroll
+            for (int v = VPL - 1; v >= 0; --v) at = key[v] == best ? (uint32_t)(v * LPT + sub) : at;
+            at = reduce<LPT>(at, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+            if (sub == k) my_id = best > none ? (int32_t)at : -1;
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
-                if ((uint32_t)(v * LPT + sub) == at) key[v] = 0;
+                if ((uint32_t)(v * LPT + sub) == at) key[v] = none;
         }
 
         const bool live = my_id >= 0;
@@ -578,13 +569,15 @@ hipError_t topk_backward_as(const void* logits, const int32_t* ids, const float*
 }
 
 // 16 lanes a token while they hold its experts in 16 elements and its slots in
-// one each; a whole wave otherwise.
-template <class LT, class F16x4, class F16x8, class F16x16, class F64x4, class F64x16>
-hipError_t choose(int E, int top_k, F16x4 a, F16x8 b, F16x16 c, F64x4 d, F64x16 e) {
+// one each; a whole wave otherwise.  Elements no expert fills cost as much as others
+// (512 experts in 8 elements a lane 11 us, in 16 16.8).
+template <class LT, class F16x4, class F16x8, class F16x16, class F64x4, class F64x8, class F64x16>
+hipError_t choose(int E, int top_k, F16x4 a, F16x8 b, F16x16 c, F64x4 d, F64x8 e, F64x16 f) {
     if (top_k <= 16 && E <= 64) return a();
     if (top_k <= 16 && E <= 128) return b();
     if (top_k <= 16 && E <= 256) return c();
-    return E <= 256 ? d() : e();
+    if (E <= 256) return d();
+    return E <= 512 ? e() : f();
 }
 
 template <class LT>
@@ -595,6 +588,7 @@ hipError_t topk_type(int score, const void* lg, const float* bias, int64_t n, in
         [&] { return topk_as<LT, 16, 8>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
         [&] { return topk_as<LT, 16, 16>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
         [&] { return topk_as<LT, 64, 4>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
+        [&] { return topk_as<LT, 64, 8>(lg, bias, n, E, k, score, rn, sc, ids, w, s); },
         [&] { return topk_as<LT, 64, 16>(lg, bias, n, E, k, score, rn, sc, ids, w, s); });
 }
 
@@ -606,6 +600,7 @@ hipError_t topk_backward_type(int score, const void* lg, const int32_t* ids, con
         [&] { return topk_backward_as<LT, 16, 8>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
         [&] { return topk_backward_as<LT, 16, 16>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
         [&] { return topk_backward_as<LT, 64, 4>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
+        [&] { return topk_backward_as<LT, 64, 8>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); },
         [&] { return topk_backward_as<LT, 64, 16>(lg, ids, dw, n, E, k, score, rn, sc, dl, s); });
 }
 

@@ -129,6 +129,20 @@ def test_topk_shapes(S, E, k, half):
         check_topk("ties" if n % 2 else "plain", S, E, k, half, score, biased, renorm, seed=S * 1000 + E + n)
 
 
+@pytest.mark.parametrize("S,E,k", [(4, 257, 8), (3, 512, 64), (5, 400, 20), (2, 513, 9), (70, 16, 16), (65, 48, 5)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_topk_ties_at_every_width(S, E, k, biased):
+    """Logits of five values and -infinity (and equal biases): the choice is the first of equals."""
+    rng = np.random.default_rng(E + k)
+    x = rng.choice(np.array([-np.inf, -3.0, -0.0, 0.0, 1.5, 2.0], np.float32), (S, E))
+    bias = torch.full((E,), 0.25, device="cuda") if biased else None
+    ids, _ = mxg.moe_topk(SIGMOID, to_gpu(x), k, bias)
+    for row, got in zip(x, ids.cpu().numpy()):
+        order = np.argsort(-row, kind="stable")
+        order = order[row[order] > -np.inf][:k]
+        assert got.tolist() == order.tolist() + [-1] * (k - len(order))
+
+
 @pytest.mark.parametrize("kind", ["plain", "ties", "masked", "lowest", "far"])
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 @pytest.mark.parametrize("biased", [False, True])
