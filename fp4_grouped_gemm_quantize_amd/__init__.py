@@ -165,13 +165,14 @@ def _expect(t: torch.Tensor, name: str, dtypes, shape=None, device=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if device is None or t.device != device:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if device is not None:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != expected {tuple(shape)}")
 
 
@@ -753,12 +754,14 @@ def _current_stream(index: int) -> int:
 
 # The handle without a Stream object around it, where torch has it: 0.1 us a call instead of 1.9.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+# The current device without the check for a lazy start (a GPU tensor is at hand): 0.14 us instead of 0.26.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(name: str, dev, *args) -> None:
     """Call the entry point `name` on dev's current stream (appended), with dev the current device."""
-    fn, index = getattr(lib(), name), dev.index
-    if index == torch.cuda.current_device():
+    fn, index = getattr(_lib or lib(), name), dev.index
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
