@@ -464,7 +464,12 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
 // workgroup's SPLIT waves share NF x 16 columns of one group and take every
 // SPLIT-th scale block of K each (together whole stretches of a weight row),
 // kDeep blocks ahead; their sums are joined in LDS in wave order.  The grid is
-// (columns, groups): no tile map, an empty group's workgroups leave at once.
+// (columns, groups): no tile map, an empty group's workgroups leave at once, the
+// others take the group's first 16 rows.  What lies past them (the host does not see
+// the group sizes) goes to `extra` more workgroups a column, first in the grid since
+// theirs is the longest way: 1024 rows of 256 groups, 2048 x 1024, all in one group
+// 36 us instead of 240 with a group's workgroups looping over its rows; even groups
+// 95 instead of 92.
 // A lane's operand pieces are 64 bytes apart (pieces kg and kg + 4 of a block),
 // so the four lanes of a row read 64 bytes together; with the nontemporal hint
 // the two halves of a line were fetched twice (K 7168, N 2048, 8 rows of 64
@@ -477,25 +482,24 @@ template <int NF, int SPLIT>
 __global__ __launch_bounds__(SPLIT * kWave, 1) void block128_rows_kernel(const GemmArgs args) {
     constexpr int kDeep = 4, kCols = NF * 16, kRows = 16, NT = SPLIT * kWave;
     __shared__ float s_sum[SPLIT][kRows][kCols + 1];
-    const int g = blockIdx.y;
-    const GroupRange gr = group_range(args.off, args.ids, g, args.T, args.E);
-    if (gr.hi <= gr.lo) return;  // workgroup-uniform
-    const int e = args.ids[g];
+    __shared__ uint32_t s_wave[SPLIT];
+    __shared__ int s_group, s_block;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), l16 = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int64_t K = args.K, N = args.N, n0 = (int64_t)blockIdx.x * kCols;
     const int nkt = (int)((K + kSB - 1) / kSB);
     const int mine = (nkt - wave + SPLIT - 1) / SPLIT;  // blocks wave, wave + SPLIT, ...
-    const uint8_t* bp[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        const int64_t n = n0 + f * 16 + l16;
-        bp[f] = args.b + ((int64_t)e * N + (n < N ? n : N - 1)) * K;  // columns past N re-read the last
-    }
-    const float* bs = static_cast<const float*>(args.bs) + ((int64_t)e * ((N + 127) / 128) + n0 / 128) * nkt;
 
-    for (int64_t m0 = gr.lo; m0 < gr.hi; m0 += kRows) {
-        const int rows_in = (int)(gr.hi - m0 < kRows ? gr.hi - m0 : kRows);
+    // rows m0 .. m0 + 15 below hi, of expert e
+    auto rows16 = [&](int e, int64_t m0, int64_t hi) {
+        const uint8_t* bp[NF];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const int64_t n = n0 + f * 16 + l16;
+            bp[f] = args.b + ((int64_t)e * N + (n < N ? n : N - 1)) * K;  // columns past N re-read the last
+        }
+        const float* bs = static_cast<const float*>(args.bs) + ((int64_t)e * ((N + 127) / 128) + n0 / 128) * nkt;
+        const int rows_in = (int)(hi - m0 < kRows ? hi - m0 : kRows);
         const int64_t r = m0 + (l16 < rows_in ? l16 : rows_in - 1);  // rows past the group re-read its last
         const uint8_t* ap = args.a + r * K;
         const float* sp = static_cast<const float*>(args.as) + r * nkt;
@@ -575,16 +579,63 @@ __global__ __launch_bounds__(SPLIT * kWave, 1) void block128_rows_kernel(const G
             if (n0 + col < N) args.c[(m0 + row) * N + n0 + col] = (uint16_t)f32_to_bf16(v);
         }
         __syncthreads();  // the sums are written again for the next rows
+    };
+
+    const int G = args.G, extra = (int)gridDim.y - G;  // extra 0: each group's workgroups take all of its rows
+    if ((int)blockIdx.y >= extra) {
+        const int g = (int)blockIdx.y - extra;
+        const GroupRange gr = group_range(args.off, args.ids, g, args.T, args.E);
+        if (gr.hi <= gr.lo) return;  // workgroup-uniform
+        const int e = args.ids[g];
+        int64_t m0 = gr.lo;
+        do rows16(e, m0, gr.hi);
+        while (extra == 0 && (m0 += kRows) < gr.hi);
+        return;
+    }
+    // The blocks of 16 rows past each group's first: the q-th of all of them, by a sum
+    // over the groups' numbers of them, kGroups consecutive groups a thread.
+    constexpr int kGroups = kMaxGroups / NT;
+    uint32_t blocks[kGroups], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int g = tid * kGroups + i;
+        blocks[i] = 0;
+        if (g < G) {
+            const GroupRange gr = group_range(args.off, args.ids, g, args.T, args.E);
+            if (gr.hi > gr.lo) blocks[i] = (uint32_t)((gr.hi - gr.lo - 1) / kRows);
+        }
+        sum += blocks[i];
+    }
+    uint32_t total;
+    const uint32_t before = block_exclusive_scan<NT>(sum, s_wave, &total);
+    for (uint32_t q = blockIdx.y; q < total; q += extra) {
+        uint32_t at = before;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            if (q >= at && q - at < blocks[i]) {
+                s_group = tid * kGroups + i;
+                s_block = (int)(q - at) + 1;
+            }
+            at += blocks[i];
+        }
+        __syncthreads();
+        const int g = __builtin_amdgcn_readfirstlane(s_group);
+        const int64_t block = __builtin_amdgcn_readfirstlane(s_block);
+        const GroupRange gr = group_range(args.off, args.ids, g, args.T, args.E);
+        rows16(args.ids[g], gr.lo + block * kRows, gr.hi);  // ends with a barrier: s_group may be written again
     }
 }
 
 constexpr int kRowFrags = 2, kRowCols = kRowFrags * 16, kRowSplit = 4;
 
-hipError_t launch_rows(const GemmProblem& p, hipStream_t stream) {
+hipError_t launch_rows(const GemmProblem& p, int64_t cus, hipStream_t stream) {
     int64_t grid = 0;
     const GemmArgs a = make_args(p, 16, kRowCols, 1, 1, &grid);
-    hipLaunchKernelGGL((block128_rows_kernel<kRowFrags, kRowSplit>), dim3((unsigned)a.ntiles_n, (unsigned)p.G),
-                       dim3(kRowSplit * kWave), 0, stream, a);
+    // the first rows of the grid take what lies past 16 rows in a group: as many as
+    // fill the chip, fewer where T holds fewer blocks
+    const int64_t fill = (2 * cus + a.ntiles_n - 1) / a.ntiles_n, extra = p.T / 16 < fill ? p.T / 16 : fill;
+    const dim3 blocks((unsigned)a.ntiles_n, (unsigned)(p.G + extra));
+    hipLaunchKernelGGL((block128_rows_kernel<kRowFrags, kRowSplit>), blocks, dim3(kRowSplit * kWave), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -628,10 +679,14 @@ hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream
     const int64_t c256 = 66 * rounds(256, 256), c128 = 44 * rounds(128, 256), c32 = 24 * rounds(32, 128);
     // The row kernel reads an expert's weights once per 16 rows: 2 rows a group
     // 133 us against 147 for the tiles, 4 rows 159 against 164, 8 rows 177 against
-    // 168 (64 experts, 7168 x 2048); where the 32 x 128 tiles do not fill the chip
-    // it still wins at 8 rows (8 experts, 2048 x 1024: 10.6 us against 14.5).
+    // 168 (64 experts, 7168 x 2048; 4 rows of 64, 4096 x 2048: 92 against 120).  One
+    // long group among short ones: 512 rows of 128, 127 in the longest, 116 against
+    // 141; 1024 of 256, 256 in it, 73 against 63 (7168 x 2048: 452 against 378).
+    // Where the 32 x 128 tiles do not fill the chip it still wins at 8 rows (8
+    // experts, 2048 x 1024: 10.6 us against 14.5).
     const bool wide_grid = (p.N + kRowCols - 1) / kRowCols * p.G < (1 << 22);
-    if (wide_grid && (rows <= 4 || (rows <= 16 && (p.N + 127) / 128 * groups < cus))) return launch_rows(p, stream);
+    const bool few = avg <= 4 && hint <= 128, small = rows <= 16 && (p.N + 127) / 128 * groups < cus;
+    if (wide_grid && (few || small)) return launch_rows(p, cus, stream);
     if (c32 < c128 && c32 < c256) return launch_tile<TileSmall>(p, stream, 1 << 30);
     if (c128 <= c256) return launch_tile<TileMid>(p, stream, 4);
     return launch_tile<TileLarge>(p, stream, 4);

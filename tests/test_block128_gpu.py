@@ -296,6 +296,31 @@ def test_gemm_many_groups():
     check_gemm(int(off[-1]), 7, 136, 160, off, rng.integers(0, 7, G))
 
 
+@pytest.mark.parametrize("law", ["one", "two", "falling", "edges"])
+@pytest.mark.parametrize("T,G,N,K", [(256, 64, 520, 416), (900, 256, 1024, 128), (4096, 1024, 1000, 96), (17, 5, 33, 64),
+                                     (60, 16, 64, 1184)])
+def test_gemm_few_rows_unevenly(T, G, N, K, law):
+    """Few rows a group on average, many in some: what lies past 16 rows of a group, past the
+    groups the grid holds at once, and a last block of one row."""
+    rng = np.random.default_rng(T + G)
+    sizes = np.zeros(G, np.int64)
+    if law == "one":
+        sizes[G // 2] = T
+    elif law == "two":
+        sizes[[0, G - 1]] = T // 2, T - T // 2
+    elif law == "falling":
+        p = (1.0 + np.arange(G)) ** -1.3
+        sizes = rng.multinomial(T, p / p.sum())
+    else:
+        left = T
+        for i, n in enumerate((16, 17, 15, 32, 33, 1, 0, 48, 49)):
+            if i < G and n <= left:
+                sizes[i] = n
+                left -= n
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    check_gemm(T, 5, N, K, off, rng.integers(-1, 6, G), seed=K)
+
+
 @pytest.mark.parametrize("most,N,K", [(128, 256, 160), (391, 512, 32)])
 def test_gemm_many_groups_of_larger_tiles(most, N, K):
     """As many groups as there may be, of 0 to `most` rows: the 128- and the 256-row tiles."""
