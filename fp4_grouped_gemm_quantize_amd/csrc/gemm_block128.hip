@@ -142,6 +142,12 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     __shared__ uint32_t s_wave[NW];
 
     constexpr bool kFresh = TM * TN * 4 >= 128;
+    // Rows a multiple of 4096 bytes apart begin in the same memory channels, and tiles
+    // side by side walk them in step: there each expert begins at a block of its own
+    // (such K have no short last block).  For the 128-row tile, which the sizes bound
+    // by the weights get: 4096 rows of 64 experts, 4096 x 2048, 137 -> 108 us; the
+    // 256-row tile gains nothing (65536 rows) or loses 2 % (8192^3).
+    constexpr bool kTurn = BM == 128;
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wm = wave / TL::WGN, wn = wave % TL::WGN;
@@ -214,6 +220,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     Coord pc{};
     next_item(pw, pc);
     int pk = 0;          // its next stage
+    int pfirst = 0;      // the block of K its stages begin with
     int pslot = 0;       // ring slot that stage goes to
     int pchunk = 0;      // scale buffer of its chunk
     const int ring0 = (int)lds_addr(s_ring), scl0 = (int)lds_addr(s_scl);
@@ -223,8 +230,9 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         const int lane = lane_id<kFresh>();
         const int r0 = wave * 8 + lane / 8;              // row of this lane in load 0 (+ 8 NW per load)
         const int chunk = swz_chunk<kSB>(r0, lane % 8);  // 16-byte piece it fetches: the swizzle
-        p_a = args.a + pc.m0 * K;
-        p_b = args.b + ((int64_t)pc.e * args.N + pc.n0) * K;
+        if constexpr (kTurn) pfirst = K % 4096 == 0 ? pc.e % nkt : 0;
+        p_a = args.a + pc.m0 * K + pfirst * kSB;
+        p_b = args.b + ((int64_t)pc.e * args.N + pc.n0) * K + pfirst * kSB;
         // rows past the group and columns past N re-read the last real one
 #pragma unroll
         for (int j = 0; j < A_J; ++j) {
@@ -254,14 +262,17 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
         const int slot = ring0 + pslot * kStage + wave * 1024;
         lds_dma16_rows<A_J, NW * 1024>(p_a, a_off, slot);
         lds_dma16_rows<B_J, NW * 1024>(p_b, b_off, slot + kAStage);
-        p_a += kSB;
-        p_b += kSB;
+        // around the end of K (where nothing turns this is the tile's end: unused)
+        const int64_t step = kTurn && pk + pfirst + 1 == nkt ? kSB - K : kSB;
+        p_a += step;
+        p_b += step;
         int issued = A_J + B_J;
         if (pk % kSclBlocks == 0) {
             pchunk = pchunk + 1 < kSlots ? pchunk + 1 : 0;
             const int dst = scl0 + pchunk * kScl;
-            // kSclBlocks blocks of each of 64 / kSclBlocks rows per load; blocks past the last re-read it
-            const int lane = lane_id<kFresh>(), blk = pk + lane % kSclBlocks;
+            // kSclBlocks blocks of each of 64 / kSclBlocks rows per load
+            const int lane = lane_id<kFresh>(), turn = pk + pfirst + lane % kSclBlocks;
+            const int blk = kTurn && turn >= nkt ? turn - nkt : turn;  // past the last without a turn: not used
             const uint32_t col = (uint32_t)(blk < nkt ? blk : nkt - 1);
             const float* as = static_cast<const float*>(args.as) + pc.m0 * nkt;
 #pragma unroll

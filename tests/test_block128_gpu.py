@@ -296,6 +296,15 @@ def test_gemm_many_groups():
     check_gemm(int(off[-1]), 7, 136, 160, off, rng.integers(0, 7, G))
 
 
+@pytest.mark.parametrize("K", [4096, 8192, 4128])
+@pytest.mark.parametrize("T,E,N", [(1500, 40, 520), (4100, 3, 1000), (40, 2, 264)])
+def test_gemm_rows_of_whole_pages(K, T, E, N):
+    """Rows a multiple of 4096 bytes apart, where tiles begin each at another block of K."""
+    rng = np.random.default_rng(K + T)
+    off = np.concatenate([[0], np.sort(rng.integers(0, T + 1, E - 1)), [T]])
+    check_gemm(T, E, N, K, off, rng.permutation(E), seed=T)
+
+
 @pytest.mark.parametrize("law", ["one", "two", "falling", "edges"])
 @pytest.mark.parametrize("T,G,N,K", [(256, 64, 520, 416), (900, 256, 1024, 128), (4096, 1024, 1000, 96), (17, 5, 33, 64),
                                      (60, 16, 64, 1184)])
