@@ -685,14 +685,14 @@ hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream
     // of 32 x 128 tiles 20 to 25; the fewest weighted rounds win.  Measured on
     // operands that no cache holds (us, 256 / 128 / 32 rows a tile): 65536 rows of
     // 128 uneven experts, 4096 x 1536: 500 / 602 / 1826; 5003 of 24, 2080 x 1000:
-    // 51 / 34 / 73; 4096 of 64, 4096 x 2048: 153 / 138 / 197; 256 of 4, 4096 x
+    // 51 / 34 / 73; 4096 of 64, 4096 x 2048: 153 / 108 / 197; 256 of 4, 4096 x
     // 2048: - / 38 / 23; 400 of 2: - / 38 / 23.
     const int64_t c256 = 66 * rounds(256, 256), c128 = 44 * rounds(128, 256), c32 = 24 * rounds(32, 128);
     // The row kernel reads an expert's weights once per 16 rows: 2 rows a group
     // 133 us against 147 for the tiles, 4 rows 159 against 164, 8 rows 177 against
-    // 168 (64 experts, 7168 x 2048; 4 rows of 64, 4096 x 2048: 92 against 120).  One
-    // long group among short ones: 512 rows of 128, 127 in the longest, 116 against
-    // 141; 1024 of 256, 256 in it, 73 against 63 (7168 x 2048: 452 against 378).
+    // 168 (64 experts, 7168 x 2048).  One long group among short ones: 512 rows of
+    // 128, 146 in the longest, 4096 x 1536, 121 against 123; 1024 of 256, 256 in it,
+    // 2048 x 1024, 73 against 63.
     // Where the 32 x 128 tiles do not fill the chip it still wins at 8 rows (8
     // experts, 2048 x 1024: 10.6 us against 14.5).
     const bool wide_grid = (p.N + kRowCols - 1) / kRowCols * p.G < (1 << 22);
