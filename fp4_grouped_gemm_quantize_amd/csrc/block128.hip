@@ -88,9 +88,10 @@ __device__ __forceinline__ void load_offsets(uint32_t* s_off, const uint32_t* of
 }
 
 // ---------------------------------------------------------------------------
-// Rows of bf16.  A unit is a row's segment of kNC 512-element chunks; loads and
-// codes are nontemporal (8192 x 4096 scattered to 65536 rows: 69 us, 5.0 TB/s; 72
-// with ordinary stores).
+// Rows of bf16.  A unit is a row's segment of kNC 512-element chunks; the codes are
+// nontemporal (8192 x 4096 scattered to 65536 rows: 67 us, 5.1 TB/s; 72 with ordinary
+// stores), the loads are not: 55 us where the last-level cache still holds the rows,
+// 68 with nontemporal loads in either case.
 // SCATTER: unit rows are tokens, encoded once and stored to the rows of the
 // token's slots (top_k <= 64: lane k holds slot k).
 constexpr int kNC = 2;
@@ -112,7 +113,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
         const int64_t e0 = (u - r * nseg) * (kNC * kChunk) + lane * 8;
 #pragma unroll
         for (int c = 0; c < kNC; ++c)
-            v[c] = e0 + c * kChunk < K ? load_stream16(x + r * K + e0 + c * kChunk) : make_uint4(0, 0, 0, 0);
+            v[c] = e0 + c * kChunk < K ? *reinterpret_cast<const uint4*>(x + r * K + e0 + c * kChunk)
+                                       : make_uint4(0, 0, 0, 0);
     };
     uint4 v[kNC];
     for (int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave; u < units; u += step) {
@@ -255,8 +257,8 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
 }
 
 // A unit is 512 outputs of a row: a lane's 8 outputs are 16 of h (two 16-byte
-// loads), 16 lanes a block; all nontemporal (32768 x 2048: 68 us, 4.9 TB/s; 72
-// with ordinary stores).
+// loads), 16 lanes a block; the codes are nontemporal (32768 x 2048: 67 us, 5.0
+// TB/s; 72 with ordinary stores, 69 with nontemporal loads).
 __global__ __launch_bounds__(kThreads) void silu_quantize_kernel(const uint16_t* __restrict__ h,
                                                                  uint8_t* __restrict__ q, float* __restrict__ scales,
                                                                  const uint32_t* __restrict__ off, int G, int64_t T,
@@ -271,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void silu_quantize_kernel(const uint16_t*
         const bool in = j < I;
         const uint16_t* p = h + r * 2 * I + 2 * j;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) v[c] = in ? load_stream16(p + 8 * c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 2; ++c) v[c] = in ? *reinterpret_cast<const uint4*>(p + 8 * c) : make_uint4(0, 0, 0, 0);
     };
     uint4 v[2];
     for (int64_t u = (int64_t)blockIdx.x * kWavesPerBlock + wave; u < units; u += step) {

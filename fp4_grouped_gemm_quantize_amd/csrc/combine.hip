@@ -93,8 +93,11 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __res
 
 // The permutation, token-major: a wave reads one segment of a token's row once
 // and stores it to the row of each of the token's slots (read once per slot the
-// same rows would cross the fabric top_k times).  Bound by the stores: 8192 x 8
-// rows of 4096 122 us, 5.0 TB/s of which eight ninths are writes.
+// same rows would cross the fabric top_k times).  Bound by the stores, which are
+// nontemporal: 8192 x 8 rows of 4096 122 us, 5.0 TB/s of which eight ninths are
+// writes, and 106 where the last-level cache still holds the tokens.  (Ordinary
+// stores 128; nontemporal loads 122 in either case; 2 and 8 KB a wave and slot
+// instead of 4 no faster.)
 constexpr int kSeg = 4;  // 16-byte vectors per lane per segment: 2048 elements a wave
 
 __global__ __launch_bounds__(kThreads) void permute_kernel(const uint16_t* __restrict__ x, int64_t ntok, int64_t H,
@@ -107,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(const uint16_t* __res
         uint4 v[kSeg];
 #pragma unroll
         for (int c = 0; c < kSeg; ++c)
-            if (u0 + c * kWave < nunits) v[c] = load_stream16(x + t * H + (u0 + c * kWave) * 8);
+            if (u0 + c * kWave < nunits) v[c] = *reinterpret_cast<const uint4*>(x + t * H + (u0 + c * kWave) * 8);
         for (int k0 = 0; k0 < top_k; k0 += kWave) {
             const int32_t mine = k0 + lane < top_k ? row_of_slot[t * top_k + k0 + lane] : -1;
             const int kn = top_k - k0 < kWave ? top_k - k0 : kWave;
