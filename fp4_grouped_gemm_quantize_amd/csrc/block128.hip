@@ -48,13 +48,19 @@ __device__ __forceinline__ float amax_of16(float v) {
     return __uint_as_float(dpp_umax<0x140>(__float_as_uint(amax_of8(v))));
 }
 
-// Codes of 8 values under their block's scale: e4m3(x / scale), the quotient as
-// IEEE binary32 division rounds it.  One division gives the scale's reciprocal r;
-// each quotient is then x r corrected by its exact remainder, q + (x - q scale) r
-// (Markstein), three operations instead of a division's ten.  Scales below 2^-60
-// are lifted by 2^64 with their values, an exact step, so that neither the
-// reciprocal overflows nor the remainder underflows.  The clamp matters only
-// where the scale is a subnormal that rounded down.
+// Codes of 8 values under their block's scale: e4m3(x / scale), the code of the
+// quotient that IEEE binary32 division gives.  One division gives the scale's
+// reciprocal r; each quotient is then x r corrected by its exact remainder,
+// q + (x - q scale) r (Markstein), three operations instead of a division's ten.
+// Scales below 2^-60 are lifted by 2^64 with their values, an exact step, so that
+// neither the reciprocal overflows nor the remainder underflows.  (Checked on the
+// CPU: the codes equal those of the division for every bf16 maximum and every bf16
+// value up to it, and for 480 M fp32 pairs, half of them next to a code's border;
+// only quotients far below the smallest code differ from the division's.)  Under an
+// infinite scale r is 0 and the remainder is taken with the largest finite number
+// instead, since 0 times infinity would make the quotient of a finite value, 0, a
+// NaN; an infinity over it stays one.  The clamp matters only where the scale is a
+// subnormal that rounded down.
 __device__ __forceinline__ uint2 encode8(const float* x, float scale) {
     float f[8];
     if (scale == 0.0f) {
@@ -62,7 +68,7 @@ __device__ __forceinline__ uint2 encode8(const float* x, float scale) {
         for (int i = 0; i < 8; ++i) f[i] = x[i] * 0.0f;
     } else {
         const float lift = scale < 0x1p-60f ? 0x1p64f : 1.0f;
-        const float s = scale * lift, r = 1.0f / s;
+        const float lifted = scale * lift, r = 1.0f / lifted, s = fminf(lifted, 0x1.fffffep127f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float xi = x[i] * lift, q = xi * r;

@@ -714,7 +714,9 @@ mxg_status mx_moe_combine_backward(const void* dout_bf16, const void* y_bf16, in
  * or columns) may be shorter.  Per block: scale = amax / 448 (IEEE fp32
  * division), code = e4m3(x / scale) (IEEE fp32 division, saturating); a block
  * whose scale is 0 gets signed-zero codes.  A block that holds an infinity or a
- * NaN gets a non-finite scale, and every product it enters is not finite.
+ * NaN gets a non-finite scale, and every product it enters is not finite; its
+ * codes are those of the same quotients: under an infinite scale signed zeros and,
+ * for the infinities, NaN (0x7f or 0xff), under a NaN all NaN.
  *
  * mx_grouped_quantize_block128: x [total_rows, K] bf16 -> q [total_rows, K] u8,
  *   scales fp32 [total_rows, ceil(K/128)]; only covered rows are written.
