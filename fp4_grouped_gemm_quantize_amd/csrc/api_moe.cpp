@@ -13,21 +13,29 @@ bool valid_type(int t) { return t == MXG_F32 || t == MXG_BF16; }
 bool valid_score(int s) { return s == MXG_SCORE_SOFTMAX || s == MXG_SCORE_SIGMOID; }
 uintptr_t type_bytes(int t) { return t == MXG_F32 ? 4 : 2; }
 
-// With MXG_VALIDATE set: refuse a row_of_slot that names a row of [0, T) twice
-// (the entry points that write rows through it).
-mxg_status check_distinct_rows(const int32_t* row_of_slot, int64_t nslots, int64_t T, hipStream_t stream) {
+// With MXG_VALIDATE set: refuse a row_of_slot that names a row twice (the entry
+// points that write rows through it).  The rows are [0, T), or with off those that
+// its G groups cover: [off[0], off[G]), since check_routing has seen that the offsets
+// rise and stay within T.
+mxg_status check_distinct_rows(const int32_t* row_of_slot, int64_t nslots, int64_t T, hipStream_t stream,
+                               const uint32_t* off = nullptr, int32_t G = 0) {
     if (!validation_on()) return MXG_SUCCESS;
     t_validation_msg[0] = '\0';
     try {
         std::vector<int32_t> h((size_t)nslots);
+        uint32_t ends[2] = {0, 0};
         if (hipMemcpyAsync(h.data(), row_of_slot, sizeof(int32_t) * h.size(), hipMemcpyDeviceToHost, stream) !=
                 hipSuccess ||
+            (off != nullptr &&
+             (hipMemcpyAsync(&ends[0], off, sizeof ends[0], hipMemcpyDeviceToHost, stream) != hipSuccess ||
+              hipMemcpyAsync(&ends[1], off + G, sizeof ends[1], hipMemcpyDeviceToHost, stream) != hipSuccess)) ||
             hipStreamSynchronize(stream) != hipSuccess)
             return MXG_ERROR_LAUNCH;
-        std::vector<bool> seen((size_t)(T < INT32_MAX ? T : (int64_t)INT32_MAX + 1));  // what an int32 can name
+        const int64_t lo = off != nullptr ? ends[0] : 0, hi = off != nullptr ? (int64_t)ends[1] : T;
+        std::vector<bool> seen((size_t)(hi < INT32_MAX ? hi : (int64_t)INT32_MAX + 1));  // what an int32 can name
         for (int64_t i = 0; i < nslots; ++i) {
             const int64_t r = h[(size_t)i];
-            if (r < 0 || r >= T) continue;
+            if (r < lo || r >= hi) continue;
             if (seen[(size_t)r]) {
                 snprintf(t_validation_msg, sizeof t_validation_msg, "row_of_slot[%lld] = %lld names a row again",
                          (long long)i, (long long)r);
@@ -164,6 +172,9 @@ mxg_status mx_grouped_quantize_block128_scatter(const void* x_tokens, int64_t nu
         !aligned(row_of_slot, 4))
         return MXG_ERROR_INVALID_VALUE;
     if (mxg_status st = check_routing(row_offsets, nullptr, num_groups, 0, total_rows, stream)) return st;
+    if (mxg_status st = check_distinct_rows(row_of_slot, num_tokens * top_k, total_rows, stream, row_offsets,
+                                            num_groups))
+        return st;
     return from_hip(mxg::launch_quantize_block128(x_tokens, num_tokens, row_of_slot, top_k, q, scales, row_offsets,
                                                   num_groups, total_rows, K, stream));
 }

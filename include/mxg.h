@@ -204,7 +204,8 @@ mxg_status mx_grouped_quantize_gather(mxg_format fmt, const void* x_bf16, int64_
  *   row_of_slot  int32 [num_tokens * top_k], device: the routed row of slot
  *                (token s, k).  Slots naming a row outside [0, total_rows)
  *                or a row no group covers are dropped.  A routed row named
- *                by several slots receives one of their results.
+ *                by several slots receives parts of their results, in no
+ *                fixed order (several waves store a row).
  *   top_k        slots per token, 1 .. 64.
  *   q, scales, row_offsets, expert_ids, num_groups, total_rows, K, stream:
  *                as in mx_grouped_quantize; routed rows no slot names are
@@ -684,10 +685,11 @@ mxg_status mx_moe_sort(const int32_t* topk_ids, int64_t num_tokens, int32_t top_
  * Rows that no slot names are left untouched.  Sums are kept in fp32 in a fixed
  * order and rounded once; no atomics.  Outputs may not overlap inputs.
  * permute and combine_backward take a row_of_slot that names no row twice, as
- * mx_moe_sort writes it: a row named by several slots receives one of their
- * values.  With MXG_VALIDATE set they read row_of_slot back and refuse a
- * repeated row (INVALID_VALUE, mxg_validation_message()).  permute_backward adds
- * such a row for each slot that names it.
+ * mx_moe_sort writes it: a row named by several slots receives parts of their
+ * values, in no fixed order (several waves store a row).  With MXG_VALIDATE set
+ * they read row_of_slot back and refuse a repeated row (INVALID_VALUE,
+ * mxg_validation_message()).  permute_backward adds such a row for each slot that
+ * names it.
  *
  * Errors: INVALID_VALUE for H <= 0, total_rows < 0, num_tokens < 0, top_k < 1,
  * a null pointer (the [total_rows, H] tensors may be null with total_rows == 0)
@@ -722,7 +724,9 @@ mxg_status mx_moe_combine_backward(const void* dout_bf16, const void* y_bf16, in
  *   scales fp32 [total_rows, ceil(K/128)]; only covered rows are written.
  * mx_grouped_quantize_block128_scatter: the token-major form, as
  *   mx_grouped_quantize_scatter: each token row is read and quantized once into
- *   its routed rows.
+ *   its routed rows.  row_of_slot names no covered row twice, as mx_moe_sort
+ *   writes it (such a row's codes and scales can come from different tokens);
+ *   with MXG_VALIDATE set a repeated one is refused, as in mx_moe_permute.
  * mx_quantize_weights_block128: w [num_experts, N, K] bf16 -> q [num_experts, N,
  *   K] u8, scales fp32 [num_experts, ceil(N/128), ceil(K/128)], and, where q_t
  *   and scales_t are given (both or neither), the transposed weights q_t
