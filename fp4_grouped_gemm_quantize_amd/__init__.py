@@ -52,7 +52,7 @@ EXPORTED = ("mx_grouped_quantize", "mx_grouped_quantize_gather", "mx_grouped_qua
             "mx_moe_sort", "mx_moe_permute", "mx_moe_permute_backward", "mx_moe_combine_backward",
             "mx_grouped_quantize_block128", "mx_grouped_quantize_block128_scatter", "mx_quantize_weights_block128",
             "mx_grouped_matmul_block128", "mx_silu_quantize_block128", "mx_silu_backward_block128", "mxg_clock_probe",
-            "mxg_fp8_tile", "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
+            "mxg_fp8_tile", "mxg_block128_tile", "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
 
 
 class MxgError(RuntimeError):
@@ -137,6 +137,8 @@ def lib() -> ctypes.CDLL:
         L.mxg_clock_probe.restype = ctypes.c_int
         L.mxg_fp8_tile.argtypes = [_I32, _I64, _I64, _I64, _I64, _I32]
         L.mxg_fp8_tile.restype = ctypes.c_int32
+        L.mxg_block128_tile.argtypes = [_I32, _I64, _I64, _I64, _I64]
+        L.mxg_block128_tile.restype = ctypes.c_int32
         L.mxg_status_string.argtypes = [ctypes.c_int]
         L.mxg_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -969,6 +971,12 @@ def mx_grouped_matmul_block128(a_q, a_scales, b_q, b_scales, c, row_offsets, exp
     _expect(expert_ids, "expert_ids", _I32T, (G,), dev)
     _run("mx_grouped_matmul_block128", dev, a_q.data_ptr(), a_scales.data_ptr(), b_q.data_ptr(), b_scales.data_ptr(),
          c.data_ptr(), row_offsets.data_ptr(), expert_ids.data_ptr(), G, E, T, N, K, int(max_rows_per_group_hint))
+
+
+def block128_tile(num_groups: int, total_rows: int, N: int, K: int, max_rows_per_group_hint: int = 0) -> int:
+    """Rows a tile of the kernel mx_grouped_matmul_block128 runs for these sizes: 256, 128, 32,
+    16 (the kernel of few rows a group), 0 (nothing / refused)."""
+    return int(lib().mxg_block128_tile(int(num_groups), int(total_rows), int(N), int(K), int(max_rows_per_group_hint)))
 
 
 def mx_silu_quantize_block128(h, y_q, y_scales, row_offsets) -> None:

@@ -637,6 +637,11 @@ __global__ __launch_bounds__(SPLIT * kWave, 1) void block128_rows_kernel(const G
     }
 }
 
+int64_t compute_units() {
+    const int cus = device_cus();
+    return cus > 0 ? cus : 256;
+}
+
 constexpr int kRowFrags = 2, kRowCols = kRowFrags * 16, kRowSplit = 4;
 
 hipError_t launch_rows(const GemmProblem& p, int64_t cus, hipStream_t stream) {
@@ -665,11 +670,10 @@ using TileSmall = BTile<32, 128, 1, 4, 4, 8>;
 
 }  // namespace
 
-hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream) {
-    const int cus_q = device_cus();
-    const int64_t cus = cus_q > 0 ? cus_q : 256;
+int block128_tile_choice(const GemmProblem& p) {
+    const int64_t cus = compute_units();
     const int64_t groups = p.G < p.T ? p.G : p.T;
-    if (groups <= 0) return hipSuccess;
+    if (groups <= 0) return 0;
     // Rows per group: the average, moved halfway to the host's hint of the largest.
     const int64_t avg = p.T / groups;
     const int64_t hint = p.max_rows_hint < p.T ? p.max_rows_hint : p.T;
@@ -697,10 +701,19 @@ hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream
     // experts, 2048 x 1024: 10.6 us against 14.5).
     const bool wide_grid = (p.N + kRowCols - 1) / kRowCols * p.G < (1 << 22);
     const bool few = avg <= 4 && hint <= 128, small = rows <= 16 && (p.N + 127) / 128 * groups < cus;
-    if (wide_grid && (few || small)) return launch_rows(p, cus, stream);
-    if (c32 < c128 && c32 < c256) return launch_tile<TileSmall>(p, stream, 1 << 30);
-    if (c128 <= c256) return launch_tile<TileMid>(p, stream, 4);
-    return launch_tile<TileLarge>(p, stream, 4);
+    if (wide_grid && (few || small)) return 16;
+    if (c32 < c128 && c32 < c256) return 32;
+    return c128 <= c256 ? 128 : 256;
+}
+
+hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream) {
+    switch (block128_tile_choice(p)) {
+        case 16: return launch_rows(p, compute_units(), stream);
+        case 32: return launch_tile<TileSmall>(p, stream, 1 << 30);
+        case 128: return launch_tile<TileMid>(p, stream, 4);
+        case 256: return launch_tile<TileLarge>(p, stream, 4);
+        default: return hipSuccess;  // no groups or no rows
+    }
 }
 
 }  // namespace mxg

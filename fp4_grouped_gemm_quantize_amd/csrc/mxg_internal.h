@@ -113,6 +113,8 @@ hipError_t launch_silu_quantize_block128(const void* h, void* yq, float* ys, con
 hipError_t launch_silu_backward_block128(const void* h, const void* dy, void* dh, void* dh_q, float* dh_scales,
                                          const uint32_t* off, int G, int64_t T, int64_t I, hipStream_t stream);
 hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream);
+// Rows a tile of the kernel it runs for these sizes: 256, 128, 32, 16 (the row kernel), 0 (nothing).
+int block128_tile_choice(const GemmProblem& p);
 
 // One wave: out[0] = shader-clock ticks, out[1] = 100 MHz ticks (>= ticks) of one sleep window.
 hipError_t launch_clock_probe(unsigned long long* out, unsigned long long ticks, hipStream_t stream);

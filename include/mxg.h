@@ -822,6 +822,16 @@ mxg_status mx_silu_backward_block128(const void* h_bf16, const void* dy_bf16, vo
  */
 int32_t mxg_fp8_tile(int32_t num_groups, int64_t total_rows, int64_t N, int64_t K,
                      int64_t max_rows_per_group_hint, int32_t prepared);
+
+/*
+ * mxg_block128_tile -- the rows a tile of the kernel that
+ * mx_grouped_matmul_block128 runs for these sizes: 256, 128 or 32, or 16 for the
+ * kernel of few rows a group; 0 where such a call would launch nothing or be
+ * refused.  For tuning and for tests, as mxg_fp8_tile; it depends on the device's
+ * compute units (256 are assumed where there is no device).
+ */
+int32_t mxg_block128_tile(int32_t num_groups, int64_t total_rows, int64_t N, int64_t K,
+                          int64_t max_rows_per_group_hint);
 mxg_status mxg_clock_probe(unsigned long long* out, int64_t window_us, hipStream_t stream);
 
 /*
