@@ -146,7 +146,8 @@ __global__ __launch_bounds__(TL::kThreads, 1) void block128_kernel(const GemmArg
     // side by side walk them in step: there each expert begins at a block of its own
     // (such K have no short last block).  For the 128-row tile, which the sizes bound
     // by the weights get: 4096 rows of 64 experts, 4096 x 2048, 137 -> 108 us; the
-    // 256-row tile gains nothing (65536 rows) or loses 2 % (8192^3).
+    // 256-row tile gains nothing (65536 rows) or loses 2 % (8192^3).  The sum of a
+    // row's blocks is then in an order that goes by the expert's id.
     constexpr bool kTurn = BM == 128;
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);

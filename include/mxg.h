@@ -742,8 +742,12 @@ mxg_status mx_moe_combine_backward(const void* dout_bf16, const void* y_bf16, in
  *   only covered rows written.  The gradient of its rows is the same call on the
  *   quantized gradient of c and q_t (K and N trade places).
  *   max_rows_per_group_hint as in mx_grouped_matmul: it only steers the choice
- *   of kernel.  (Kernels may join the blocks' sum in another order: the fp32
- *   sum, and so the last bit of c, can differ between two hints.)
+ *   of kernel.  A call repeated gives the same bits.  The order in which a row's
+ *   blocks are added goes by the kernel (by the sizes and the hint) and, for K a
+ *   multiple of 4096, by the expert's id: results of such calls are apart by the
+ *   rounding of the fp32 sum, at most (2 ceil(K/128) + 9) 2^-24 of its sum of
+ *   magnitudes before the rounding to bf16, which is more than the last bit of c
+ *   where the sum cancels.
  * Outputs may not overlap inputs or each other, here and below (dh_bf16 apart).
  *
  * Errors: INVALID_VALUE for null pointers, sizes <= 0 (total_rows / num_groups /

@@ -91,6 +91,32 @@ def test_kernels_agree(N, K):
     assert bool(((got - ref).abs() <= spread_of(a, sa, b[1], sb[1], slice(0, 3), got, ref)).all())
 
 
+@pytest.mark.parametrize("K", [4096, 8192])
+def test_rows_of_whole_pages(K):
+    """K a multiple of 4096: the 128-row tile begins an expert's sum at a block of K that goes by the expert's id,
+    so the same rows under the same weights of another expert, or through another kernel, differ by the order of
+    the sum and no more; the other kernels' sums do not depend on the id."""
+    N, E = 520, 6
+    a, sa, b, sb = operands(16400, E, N, K, 5)
+    b[5], sb[5] = b[0], sb[0]  # the same weights under two ids
+    a, sa, b, sb = (to_gpu(v) for v in (a, sa, b, sb))
+
+    def first3(rows_of_kernel, T, e):
+        tile_of(T, N, K, rows_of_kernel)
+        return mxg.grouped_matmul_block128(a[:T].contiguous(), sa[:T].contiguous(), b, sb,
+                                           offsets_gpu(np.array([0, T], np.uint32)), to_gpu(np.array([e], np.int32)))[:3]
+
+    sizes = {256: 16400, 128: 5000, 32: 40, 16: 3}
+    ref = first3(256, 16400, 0)
+    for rows_of_kernel, T in sizes.items():
+        c0, c5 = first3(rows_of_kernel, T, 0), first3(rows_of_kernel, T, 5)
+        if rows_of_kernel != 128:
+            assert torch.equal(c0.view(torch.int16), c5.view(torch.int16))
+        assert torch.equal(c5.view(torch.int16), first3(rows_of_kernel, T, 5).view(torch.int16))  # the same call twice
+        for c in (c0.double(), c5.double()):
+            assert bool(((c - ref.double()).abs() <= spread_of(a, sa, b[0], sb[0], slice(0, 3), c, ref.double())).all())
+
+
 @pytest.mark.parametrize("T,G,N,K", [(1000, 256, 264, 512), (40, 4, 130, 1184), (300, 100, 33, 96)])
 def test_hint_changes_the_kernel(T, G, N, K):
     assert mxg.block128_tile(G, T, N, K, 0) == 16 and mxg.block128_tile(G, T, N, K, 1 << 62) != 16
