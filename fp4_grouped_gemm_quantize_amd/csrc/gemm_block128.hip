@@ -37,8 +37,10 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kSB = 128;          // stage bytes per row: one scale block
 
-// BM tokens x BN columns, WGM x WGN waves, SLOTS ring slots (SLOTS - 1 stages in
-// flight), SCL scale blocks per LDS chunk.
+// BM tokens x BN columns, WGM x WGN waves, SLOTS ring slots (loads run SLOTS - 1
+// stages ahead; the wait at a stage's end leaves only those issued in that stage in
+// flight, so past the third slot they are early rather than more), SCL scale blocks
+// per LDS chunk.
 template <int BM_, int BN_, int WGM_, int WGN_, int SLOTS_, int SCL_>
 struct BTile {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, kSlots = SLOTS_, kScl = SCL_;

@@ -780,6 +780,7 @@ mxg_status mx_grouped_matmul_block128(const void* a_q, const float* a_scales, co
  *            of mx_silu_quantize).
  *   y_j = g_j / (1 + e^-g_j) * u_j in fp32, quantized as it is (no bf16 between)
  *            into y_q [total_rows, I] u8, y_scales fp32 [total_rows, ceil(I/128)].
+ *            (A sigmoid below fp32's normal range may count as 0, here and below.)
  *   backward: dy_bf16 [total_rows, I]; with s = 1 / (1 + e^-g), in fp32:
  *            dg = dy u s (1 + g (1 - s)), du = dy g s, interleaved as h is;
  *            kept in dh_bf16 [total_rows, 2I] (rounded once) and / or quantized
