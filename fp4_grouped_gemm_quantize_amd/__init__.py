@@ -16,10 +16,15 @@ Entry points (same names as the C ABI in include/mxg.h):
     mx_grouped_quantize_block128(x, q, scales, row_offsets)
     mx_grouped_matmul_block128(a_q, a_scales, b_q, b_scales, c, row_offsets, expert_ids, max_rows_per_group_hint=0)
     mx_silu_quantize_block128(h, y_q, y_scales, row_offsets)
-and the gradients mx_moe_topk_backward, mx_moe_permute_backward, mx_moe_combine_backward, mx_silu_backward_block128;
-plus allocating conveniences quantize(), grouped_matmul(), grouped_matmul_swiglu(), silu_quantize(), moe_topk(),
-moe_sort(), moe_permute(), quantize_block128(), quantize_weights_block128(), grouped_matmul_block128(),
-silu_quantize_block128().
+    mx_rmsnorm(x, weight, residual=None, h=None, y=None, form=NORM_PLAIN, q=None, scales=None, eps=1e-6,
+               weight_offset=0.0)
+    mx_grouped_matmul_bf16(a, b, c, row_offsets=None, expert_ids=None, bias=None, act=ACT_NONE, residual=None, z=None,
+                           max_rows_per_group_hint=0)
+and the gradients mx_moe_topk_backward, mx_moe_permute_backward, mx_moe_combine_backward, mx_silu_backward_block128,
+mx_rmsnorm_backward, mx_grouped_matmul_bf16_backward, mx_grouped_matmul_bf16_backward_weights,
+mx_activation_backward; plus allocating conveniences quantize(), grouped_matmul(), grouped_matmul_swiglu(),
+silu_quantize(), moe_topk(), moe_sort(), moe_permute(), quantize_block128(), quantize_weights_block128(),
+grouped_matmul_block128(), silu_quantize_block128(), rmsnorm(), grouped_matmul_bf16().
 """
 from __future__ import annotations
 
@@ -35,6 +40,8 @@ FORMATS = {FP8_ROWWISE: "fp8_e4m3_rowwise", MXFP8: "mxfp8_e4m3", MXFP4: "mxfp4_e
 
 F32, BF16 = 0, 1                       # mxg_dtype
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1    # mxg_score
+NORM_PLAIN, NORM_FP8_ROWWISE, NORM_MXFP8, NORM_FP8_BLOCK128 = 0, 1, 2, 3   # mxg_norm_format
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU, ACT_SWIGLU = 0, 1, 2, 3, 4         # mxg_activation
 
 SUCCESS, ERROR_INVALID_VALUE, ERROR_NOT_SUPPORTED, ERROR_LAUNCH = 0, 1, 2, 3
 MAX_GROUPS = 1024
@@ -51,7 +58,10 @@ EXPORTED = ("mx_grouped_quantize", "mx_grouped_quantize_gather", "mx_grouped_qua
             "mx_prepare_weights_fp8", "mx_grouped_matmul_prepared", "mx_moe_topk", "mx_moe_topk_backward",
             "mx_moe_sort", "mx_moe_permute", "mx_moe_permute_backward", "mx_moe_combine_backward",
             "mx_grouped_quantize_block128", "mx_grouped_quantize_block128_scatter", "mx_quantize_weights_block128",
-            "mx_grouped_matmul_block128", "mx_silu_quantize_block128", "mx_silu_backward_block128", "mxg_clock_probe",
+            "mx_grouped_matmul_block128", "mx_silu_quantize_block128", "mx_silu_backward_block128", "mx_rmsnorm",
+            "mx_rmsnorm_workspace_bytes", "mx_rmsnorm_backward", "mx_grouped_matmul_bf16",
+            "mx_grouped_matmul_bf16_backward", "mx_grouped_matmul_bf16_backward_weights", "mx_activation_backward",
+            "mxg_clock_probe",
             "mxg_fp8_tile", "mxg_block128_tile", "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
 
 
@@ -125,10 +135,23 @@ def lib() -> ctypes.CDLL:
                 ("mx_quantize_weights_block128", [_P, _I32, _I64, _I64, _P, _P, _P, _P, _P]),
                 ("mx_grouped_matmul_block128", [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I64, _I64, _I64, _I64, _P]),
                 ("mx_silu_quantize_block128", [_P, _P, _P, _P, _I32, _I64, _I64, _P]),
-                ("mx_silu_backward_block128", [_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _P])):
+                ("mx_silu_backward_block128", [_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _P]),
+                ("mx_rmsnorm", [ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int, _P, f32, f32, _I64, _I64, _P, _P,
+                                _P, _P, _P]),
+                ("mx_rmsnorm_backward", [ctypes.c_int, _P, _P, ctypes.c_int, _P, f32, f32, _P, _I64, _I64, _P, _P, _P,
+                                         _P, _P]),
+                ("mx_grouped_matmul_bf16", [ctypes.c_int, _P, _P, _P, _P, ctypes.c_int, _P, _P, _P, _P, _I32, _I32,
+                                            _I64, _I64, _I64, _I64, _P]),
+                ("mx_grouped_matmul_bf16_backward", [ctypes.c_int, _P, _P, _P, _P, _P, _P, _I32, _I32, _I64, _I64,
+                                                     _I64, _I64, _P]),
+                ("mx_grouped_matmul_bf16_backward_weights", [_P, _P, ctypes.c_int, _P, _P, _I32, _P, _P, _I32, _I32,
+                                                             _I64, _I64, _I64, _P]),
+                ("mx_activation_backward", [ctypes.c_int, _P, _P, _P, _I64, _I64, _P])):
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        L.mx_rmsnorm_workspace_bytes.argtypes = [_I64, _I64]
+        L.mx_rmsnorm_workspace_bytes.restype = ctypes.c_int64
         L.mxg_validation_message.argtypes = []
         L.mxg_validation_message.restype = ctypes.c_char_p
         L.mxg_routing_violation.argtypes = [_P, _P, _I32, _I32, _I64, ctypes.c_char_p, _I64]
@@ -1019,6 +1042,216 @@ def mx_silu_backward_block128(h, dy, row_offsets, dh=None, dh_q=None, dh_scales=
          row_offsets.data_ptr(), G, T, I)
 
 
+# ----------------------------------------------------------------------------- norm, BF16 products and their gradients
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _span(t):
+    a = t.data_ptr()
+    return a, a + t.nbytes
+
+
+def _outputs_apart(outputs, inputs) -> None:
+    """Refuse outputs that share memory with an input or another output; both are lists of (name, tensor or None)."""
+    seen = [(n, *_span(t)) for n, t in inputs if t is not None]
+    for name, t in outputs:
+        if t is None:
+            continue
+        lo, hi = _span(t)
+        for other, a, b in seen:
+            if lo < b and a < hi:
+                raise ValueError(f"{name} and {other} may not overlap")
+        seen.append((name, lo, hi))
+
+
+def _type(t) -> int:
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+def mx_rmsnorm(x, weight, residual=None, h=None, y=None, form: int = NORM_PLAIN, q=None, scales=None,
+               eps: float = 1e-6, weight_offset: float = 0.0) -> None:
+    """Root-mean-square norm of the rows of x [S, H] with the weight [H] (fp32 or bf16), after the addition of
+    residual [S, H] (fp32 or bf16; x is bf16 then), whose sum goes to h (of residual's type; may be residual):
+    y bf16 [S, H], and / or the codes q u8 [S, H] with their scales in one of the 8-bit forms
+    (NORM_FP8_ROWWISE: fp32 [S], NORM_MXFP8: u8 [S, H/32], NORM_FP8_BLOCK128: fp32 [S, ceil(H/128)])."""
+    S, H = _matrix(x, "x", _LOGITS if residual is None else _BF16)
+    dev = x.device
+    _expect(weight, "weight", _LOGITS, (H,), dev)
+    if (residual is None) != (h is None):
+        raise ValueError("residual and h go together")
+    if residual is not None:
+        _expect(residual, "residual", _LOGITS, (S, H), dev)
+        _expect(h, "h", (residual.dtype,), (S, H), dev)
+    if y is not None:
+        _expect(y, "y", _BF16, (S, H), dev)
+    if (q is None) != (form == NORM_PLAIN) or (scales is None) != (q is None):
+        raise ValueError("q and scales go with the 8-bit forms, both of them")
+    if q is not None:
+        _expect(q, "q", _U8, (S, H), dev)
+        _expect(scales, "scales", _U8 if form == NORM_MXFP8 else _F32,
+                (S,) if form == NORM_FP8_ROWWISE else (S, H // 32 if form == NORM_MXFP8 else _blocks128(H)), dev)
+    elif y is None:
+        raise ValueError("give y, or q with scales, or all three")
+    # h may be its residual or, both bf16, x
+    at = None if h is None else h.data_ptr()
+    reads = [("weight", weight)]
+    if at is None or at != x.data_ptr() or h.dtype != x.dtype:
+        reads.append(("x", x))
+    if residual is not None and at != residual.data_ptr():
+        reads.append(("residual", residual))
+    _outputs_apart((("h", h),), reads)
+    _outputs_apart((("y", y), ("q", q), ("scales", scales)), (("weight", weight), ("x", x), ("residual", residual),
+                                                               ("h", h)))
+    _run("mx_rmsnorm", dev, form, _type(x if residual is None else residual), x.data_ptr(), _opt(residual),
+         _type(weight), weight.data_ptr(), weight_offset, eps, S, H, _opt(h), _opt(y), _opt(q), _opt(scales))
+
+
+def rmsnorm_workspace_bytes(num_tokens: int, H: int) -> int:
+    """Bytes of the workspace that mx_rmsnorm_backward needs for a weight gradient."""
+    n = lib().mx_rmsnorm_workspace_bytes(num_tokens, H)
+    if n < 0:
+        raise ValueError(f"rows of {H} elements are not supported")
+    return n
+
+
+def mx_rmsnorm_backward(dy, h, weight, dx=None, dh=None, dx_bf16=None, dweight=None, workspace=None,
+                        eps: float = 1e-6, weight_offset: float = 0.0) -> None:
+    """The gradient of mx_rmsnorm from dy bf16 [S, H] and the stream h [S, H] it normed: dx [S, H] of h's type,
+    with dh (of that type; may be dx) added, dx_bf16 the same in bf16, dweight fp32 [H].  workspace: fp32, of
+    rmsnorm_workspace_bytes(S, H) bytes, for dweight (taken from torch where it is not given)."""
+    S, H = _matrix(h, "h", _LOGITS)
+    dev = h.device
+    _expect(dy, "dy", _BF16, (S, H), dev)
+    _expect(weight, "weight", _LOGITS, (H,), dev)
+    for name, t, kind in (("dh", dh, (h.dtype,)), ("dx", dx, (h.dtype,)), ("dx_bf16", dx_bf16, _BF16)):
+        if t is not None:
+            _expect(t, name, kind, (S, H), dev)
+    if dweight is not None:
+        _expect(dweight, "dweight", _F32, (H,), dev)
+        need = rmsnorm_workspace_bytes(S, H)
+        if workspace is None:
+            workspace = torch.empty((max(need // 4, 1),), dtype=torch.float32, device=dev)
+        else:
+            _expect(workspace, "workspace", _F32, None, dev)
+            if workspace.nbytes < need:
+                raise ValueError(f"workspace holds {workspace.nbytes} bytes, {need} are needed")
+    elif dx is None and dx_bf16 is None:
+        raise ValueError("give dx, dx_bf16 or dweight")
+    else:
+        workspace = None
+    apart = (("dx_bf16", dx_bf16), ("dweight", dweight), ("workspace", workspace))
+    reads = (("dy", dy), ("h", h), ("weight", weight))
+    if dx is not None and dh is not None and dx.data_ptr() == dh.data_ptr():
+        _outputs_apart((("dx", dx), *apart), reads)
+    else:
+        _outputs_apart((("dx", dx), *apart), (*reads, ("dh", dh)))
+    _run("mx_rmsnorm_backward", dev, _type(h), dy.data_ptr(), h.data_ptr(), _type(weight), weight.data_ptr(),
+         weight_offset, eps, _opt(dh), S, H, _opt(dx), _opt(dx_bf16), _opt(dweight), _opt(workspace))
+
+
+def _bf16_groups(row_offsets, expert_ids, dev):
+    """num_groups of the routing, or 1 where there is none (a dense product)."""
+    if row_offsets is None and expert_ids is None:
+        return 1
+    if row_offsets is None or expert_ids is None:
+        raise ValueError("row_offsets and expert_ids go together")
+    G = _groups(row_offsets, dev)
+    _expect(expert_ids, "expert_ids", _I32T, (G,), dev)
+    return G
+
+
+def _experts(b, dev, name: str = "b"):
+    """The sizes (E, N, K) of expert weights."""
+    _expect(b, name, _BF16, None, dev)
+    if b.dim() != 3:
+        raise ValueError(f"{name} must be [num_experts, N, K]")
+    return b.shape
+
+
+def mx_grouped_matmul_bf16(a, b, c, row_offsets=None, expert_ids=None, bias=None, act: int = ACT_NONE, residual=None,
+                           z=None, max_rows_per_group_hint: int = 0) -> None:
+    """Ragged grouped product of bf16 a [T, K] and b [E, N, K]: c = act(a b + bias) + residual, with bias fp32
+    [E, N], residual and c [T, N] (ACT_SWIGLU: [T, N/2]) in bf16 or fp32 (residual may be c), and, where z bf16
+    [T, N] is given, a b + bias kept in it.  Without routing: one dense product (E = 1)."""
+    T, K = _matrix(a, "a", _BF16)
+    dev = a.device
+    E, N, kb = _experts(b, dev)
+    if kb != K:
+        raise ValueError(f"b: rows of {kb}, expected {K}")
+    wide = N // 2 if act == ACT_SWIGLU else N
+    _expect(c, "c", _LOGITS, (T, wide), dev)
+    if bias is not None:
+        _expect(bias, "bias", _F32, (E, N), dev)
+    if residual is not None:
+        _expect(residual, "residual", (c.dtype,), (T, wide), dev)
+    if z is not None:
+        _expect(z, "z", _BF16, (T, N), dev)
+    G = _bf16_groups(row_offsets, expert_ids, dev)
+    own = residual is not None and residual.data_ptr() == c.data_ptr()
+    _outputs_apart((("c", c), ("z", z)), (("a", a), ("b", b), ("bias", bias), ("residual", None if own else residual)))
+    _run("mx_grouped_matmul_bf16", dev, act, a.data_ptr(), b.data_ptr(), _opt(bias), _opt(residual), _type(c),
+         c.data_ptr(), _opt(z), _opt(row_offsets), _opt(expert_ids), G, E, T, N, K, int(max_rows_per_group_hint))
+
+
+def mx_grouped_matmul_bf16_backward(dc, b, da, row_offsets=None, expert_ids=None, act: int = ACT_NONE, z=None,
+                                    max_rows_per_group_hint: int = 0) -> None:
+    """The gradient of the rows of mx_grouped_matmul_bf16: da [T, K] = act'(z) * (dc [T, N] b [E, N, K]), bf16;
+    act and z [T, K] are those of the product that made the rows (ACT_SWIGLU: z and da are [T, 2K]; z may be da)."""
+    T, N = _matrix(dc, "dc", _BF16)
+    dev = dc.device
+    E, nb, K = _experts(b, dev)
+    if nb != N:
+        raise ValueError(f"b: {nb} rows an expert, expected {N}")
+    wide = 2 * K if act == ACT_SWIGLU else K
+    _expect(da, "da", _BF16, (T, wide), dev)
+    if (z is None) != (act == ACT_NONE):
+        raise ValueError("z goes with an activation")
+    if z is not None:
+        _expect(z, "z", _BF16, (T, wide), dev)
+    G = _bf16_groups(row_offsets, expert_ids, dev)
+    own = z is not None and z.data_ptr() == da.data_ptr()
+    _outputs_apart((("da", da),), (("dc", dc), ("b", b), ("z", None if own else z)))
+    _run("mx_grouped_matmul_bf16_backward", dev, act, dc.data_ptr(), b.data_ptr(), _opt(z), da.data_ptr(),
+         _opt(row_offsets), _opt(expert_ids), G, E, T, N, K, int(max_rows_per_group_hint))
+
+
+def mx_grouped_matmul_bf16_backward_weights(dc, a, dw, row_offsets=None, expert_ids=None, dbias=None,
+                                            accumulate: bool = False) -> None:
+    """The gradient of the weights and bias of mx_grouped_matmul_bf16: dw [E, N, K] (fp32 or bf16) = the sum over
+    each expert's rows of dc [T, N] times a [T, K], dbias fp32 [E, N] that of dc; added to what they hold with
+    accumulate, else in its place (zeros for an expert without rows)."""
+    T, N = _matrix(dc, "dc", _BF16)
+    dev = dc.device
+    ta, K = _matrix(a, "a", _BF16, dev)
+    if ta != T:
+        raise ValueError(f"a: {ta} rows, expected {T}")
+    _expect(dw, "dw", _LOGITS, None, dev)
+    if dw.dim() != 3 or dw.shape[1] != N or dw.shape[2] != K:
+        raise ValueError(f"dw: shape {tuple(dw.shape)}, expected (num_experts, {N}, {K})")
+    E = dw.shape[0]
+    if dbias is not None:
+        _expect(dbias, "dbias", _F32, (E, N), dev)
+    G = _bf16_groups(row_offsets, expert_ids, dev)
+    _outputs_apart((("dw", dw), ("dbias", dbias)), (("dc", dc), ("a", a)))
+    _run("mx_grouped_matmul_bf16_backward_weights", dev, dc.data_ptr(), a.data_ptr(), _type(dw), dw.data_ptr(),
+         _opt(dbias), 1 if accumulate else 0, _opt(row_offsets), _opt(expert_ids), G, E, T, N, K)
+
+
+def mx_activation_backward(act: int, dc, z, dz) -> None:
+    """dz = act'(z) * dc by itself: dc [T, N], z and dz [T, N] bf16 (ACT_SWIGLU: z and dz [T, 2N]); dz may be z or,
+    without ACT_SWIGLU, dc."""
+    T, N = _matrix(dc, "dc", _BF16)
+    dev = dc.device
+    wide = 2 * N if act == ACT_SWIGLU else N
+    _expect(z, "z", _BF16, (T, wide), dev)
+    _expect(dz, "dz", _BF16, (T, wide), dev)
+    at = dz.data_ptr()
+    _outputs_apart((("dz", dz),), (("z", None if at == z.data_ptr() else z),
+                                   ("dc", None if at == dc.data_ptr() and act != ACT_SWIGLU else dc)))
+    _run("mx_activation_backward", dev, act, dc.data_ptr(), z.data_ptr(), dz.data_ptr(), T, N)
+
+
 # ----------------------------------------------------------------------------- allocating forms
 def moe_topk(score: int, logits, top_k: int, bias=None, renormalize: bool = True, scale: float = 1.0):
     """Returns (topk_ids int32 [S, top_k], topk_weights fp32 [S, top_k])."""
@@ -1079,3 +1312,26 @@ def silu_quantize_block128(h, row_offsets):
     ys = torch.zeros((T, _blocks128(I)), dtype=torch.float32, device=h.device)
     mx_silu_quantize_block128(h, yq, ys, row_offsets)
     return yq, ys
+
+
+def rmsnorm(x, weight, residual=None, form: int = NORM_PLAIN, eps: float = 1e-6, weight_offset: float = 0.0):
+    """Returns (y, h, q, scales): y bf16; h the stream with the residual added (x without one); q and scales None
+    with NORM_PLAIN."""
+    S, H = x.shape
+    e = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+    h = None if residual is None else torch.empty_like(residual)
+    q = None if form == NORM_PLAIN else e((S, H), torch.uint8)
+    scales = (None if q is None else e((S,), torch.float32) if form == NORM_FP8_ROWWISE else
+              e((S, H // 32), torch.uint8) if form == NORM_MXFP8 else e((S, _blocks128(H)), torch.float32))
+    y = e((S, H), torch.bfloat16)
+    mx_rmsnorm(x, weight, residual, h, y, form, q, scales, eps, weight_offset)
+    return y, x if h is None else h, q, scales
+
+
+def grouped_matmul_bf16(a, b, row_offsets=None, expert_ids=None, bias=None, act: int = ACT_NONE, residual=None,
+                        dtype=torch.bfloat16, max_rows_per_group_hint: int = 0):
+    """Returns c (rows no group covers are zero)."""
+    wide = b.shape[1] // 2 if act == ACT_SWIGLU else b.shape[1]
+    c = torch.zeros((a.shape[0], wide), dtype=dtype, device=a.device)
+    mx_grouped_matmul_bf16(a, b, c, row_offsets, expert_ids, bias, act, residual, None, max_rows_per_group_hint)
+    return c

@@ -19,8 +19,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxg.so")
-SOURCES = ["api.cpp", "api_moe.cpp", "api_query.cpp", "quantize.hip", "gemm.hip", "gemm_block128.hip", "block128.hip",
-           "combine.hip", "route.hip", "clock.hip"]
+SOURCES = ["api.cpp", "api_moe.cpp", "api_dense.cpp", "api_query.cpp", "quantize.hip", "gemm.hip", "gemm_block128.hip",
+           "gemm_bf16.hip", "gemm_bf16_weights.hip", "norm.hip", "block128.hip", "combine.hip", "route.hip",
+           "clock.hip"]
 ARCH = os.environ.get("MXG_OFFLOAD_ARCH", "gfx950")
 
 COMMON = [

@@ -1,0 +1,192 @@
+// gemm_bf16.h -- what the BF16 products' kernels share: the argument block, the
+// activations with their derivatives, and the epilogues of four neighbouring columns
+// of a row.  Device code for gfx950.
+#pragma once
+
+#include "mxg_device.h"
+#include "mxg_internal.h"
+
+#include <type_traits>
+
+namespace mxg {
+namespace bf16 {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+enum Act { kNone = 0, kRelu = 1, kGelu = 2, kSilu = 3, kSwiglu = 4 };  // mxg_activation
+
+// The group's rows; without routing one group of all rows.
+__device__ __forceinline__ GroupRange rows_of(const uint32_t* off, const int32_t* ids, int g, int64_t T, int E) {
+    if (off == nullptr) return {0, T};
+    return group_range(off, ids, g, T, E);
+}
+__device__ __forceinline__ int expert_of(const int32_t* ids, int g) { return ids == nullptr ? 0 : ids[g]; }
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// The normal distribution's Phi(z), by erfc so that it keeps its digits where it is small.
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;  // keeps a NaN
+    if constexpr (ACT == kGelu) return z * normal_cdf(z);
+    if constexpr (ACT == kSilu) return z / (1.0f + expf(-z));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float derivative(float z) {
+    if constexpr (ACT == kRelu) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == kGelu) return fmaf(z, 0.39894228040143268f * expf(-0.5f * z * z), normal_cdf(z));
+    if constexpr (ACT == kSilu) {
+        const float s = sigmoid(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    return 1.0f;
+}
+// Runs f with the activation as a constant.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+    switch (act) {
+        case kRelu: f(std::integral_constant<int, kRelu>{}); break;
+        case kGelu: f(std::integral_constant<int, kGelu>{}); break;
+        case kSilu: f(std::integral_constant<int, kSilu>{}); break;
+        case kSwiglu: f(std::integral_constant<int, kSwiglu>{}); break;
+        default: f(std::integral_constant<int, kNone>{}); break;
+    }
+}
+
+// W neighbouring elements at p (fp32 or bf16): whole (aligned to W elements), or the first n.
+template <int W>
+__device__ __forceinline__ void load_n(const void* p, bool f32, bool whole, int n, float* v) {
+    if (f32) {
+        const float* q = static_cast<const float*>(p);
+        if (whole) {
+            typedef float vt __attribute__((ext_vector_type(W)));
+            const vt x = *reinterpret_cast<const vt*>(q);
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = x[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = i < n ? q[i] : 0.0f;
+        }
+    } else {
+        const uint16_t* q = static_cast<const uint16_t*>(p);
+        if (whole) {
+            typedef uint16_t vt __attribute__((ext_vector_type(W)));
+            const vt x = *reinterpret_cast<const vt*>(q);
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = bf16_to_f32(x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = i < n ? bf16_to_f32(q[i]) : 0.0f;
+        }
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_n(void* p, bool f32, bool whole, int n, const float* v) {
+    if (f32) {
+        float* q = static_cast<float*>(p);
+        if (whole) {
+            typedef float vt __attribute__((ext_vector_type(W)));
+            vt x;
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[i] = v[i];
+            *reinterpret_cast<vt*>(q) = x;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (i < n) q[i] = v[i];
+        }
+    } else {
+        uint16_t* q = static_cast<uint16_t*>(p);
+        if (whole) {
+            uint32_t x[W / 2];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) x[i] = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
+            __builtin_memcpy(__builtin_assume_aligned(q, 2 * W), x, 2 * W);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (i < n) q[i] = (uint16_t)f32_to_bf16(v[i]);
+        }
+    }
+}
+
+// The forward epilogue of columns col .. col + 3 (those below N) of row t of expert e,
+// from the sums v.
+template <int ACT>
+__device__ __forceinline__ void finish4(const Bf16Problem& p, int e, int64_t t, int64_t col, const float* sums) {
+    const int n = (int)(p.N - col < 4 ? p.N - col : 4);
+    const bool whole = (p.N & 3) == 0;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = sums[i];
+    if (p.bias) {
+        float b[4];
+        load_n<4>(p.bias + e * p.N + col, true, false, n, b);  // bias is aligned to its elements only
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += b[i];
+    }
+    if (p.z) store_n<4>(static_cast<uint16_t*>(p.z) + t * p.N + col, false, whole, n, v);
+    const int size = p.c32 ? 4 : 2;
+    if constexpr (ACT == kSwiglu) {
+        float y[2] = {activate<kSilu>(v[0]) * v[1], activate<kSilu>(v[2]) * v[3]};
+        const int64_t at = (t * (p.N / 2) + col / 2) * size;
+        if (p.res) {
+            float r[2];
+            load_n<2>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n / 2, r);
+            y[0] += r[0];
+            y[1] += r[1];
+        }
+        store_n<2>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n / 2, y);
+    } else {
+        const int64_t at = (t * p.N + col) * size;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+        if (p.res) {
+            float r[4];
+            load_n<4>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += r[i];
+        }
+        store_n<4>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n, v);
+    }
+}
+
+// d times the derivative at z, eight columns (swiglu: of four sums).
+__device__ __forceinline__ void swiglu_grad4(const float* z, const float* d, float* out) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float g = z[2 * i], u = z[2 * i + 1], s = sigmoid(g);
+        out[2 * i] = d[i] * u * s * (1.0f + g * (1.0f - s));
+        out[2 * i + 1] = d[i] * g * s;
+    }
+}
+
+// The backward epilogue of columns col .. col + 3 of row t (K is a multiple of 8: all of them).
+template <int ACT>
+__device__ __forceinline__ void finish4_backward(const Bf16Problem& p, int64_t t, int64_t col, const float* d) {
+    if constexpr (ACT == kSwiglu) {
+        const int64_t at = (t * p.K + col) * 2;
+        float z[8], out[8];
+        load_n<8>(static_cast<const uint16_t*>(p.z) + at, false, true, 8, z);
+        swiglu_grad4(z, d, out);
+        store_n<8>(static_cast<uint16_t*>(p.c) + at, false, true, 8, out);
+    } else {
+        const int64_t at = t * p.K + col;
+        float v[4];
+        if constexpr (ACT == kNone) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = d[i];
+        } else {
+            load_n<4>(static_cast<const uint16_t*>(p.z) + at, false, true, 4, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = d[i] * derivative<ACT>(v[i]);
+        }
+        store_n<4>(static_cast<uint16_t*>(p.c) + at, false, true, 4, v);
+    }
+}
+
+}  // namespace bf16
+}  // namespace mxg

@@ -116,6 +116,43 @@ hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream
 // Rows a tile of the kernel it runs for these sizes: 256, 128, 32, 16 (the row kernel), 0 (nothing).
 int block128_tile_choice(const GemmProblem& p);
 
+// The norm of a residual stream and its gradient (norm.hip).  fmt: mxg_norm_format; s32, w32: fp32 stream, weight.
+hipError_t launch_rmsnorm(int fmt, bool s32, const void* x, const void* res, bool w32, const void* w, float w_add,
+                          float eps, int64_t T, int64_t H, void* h, void* y, void* q, void* scales,
+                          hipStream_t stream);
+int64_t rmsnorm_workspace_rows(int64_t T, int64_t H);  // of H floats each
+hipError_t launch_rmsnorm_backward(bool s32, const void* dy, const void* h, bool w32, const void* w, float w_add,
+                                   float eps, const void* dh, int64_t T, int64_t H, void* dx, void* dx_bf16,
+                                   float* dw, float* ws, hipStream_t stream);
+
+// BF16 products and their gradients (gemm_bf16.hip, gemm_bf16_weights.hip).  off == nullptr (with ids): one group
+// of all T rows, expert 0.  act: mxg_activation.
+struct Bf16Problem {
+    int act;
+    const void* a;      // [T, K]; backward: dc [T, N]
+    const void* b;      // [E, N, K]
+    const float* bias;  // [E, N] or nullptr
+    const void* res;    // as c, or nullptr
+    void* c;            // backward: da
+    bool c32;           // c and res in fp32
+    void* z;            // forward: kept pre-activations or nullptr; backward: those of act
+    const uint32_t* off;
+    const int32_t* ids;
+    int G;
+    int E;
+    int64_t T;
+    int64_t N;
+    int64_t K;
+    int64_t max_rows_hint;
+};
+hipError_t launch_matmul_bf16(const Bf16Problem& p, hipStream_t stream);
+hipError_t launch_matmul_bf16_backward(const Bf16Problem& p, hipStream_t stream);
+hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, bool dw32, float* dbias,
+                                      bool accumulate, const uint32_t* off, const int32_t* ids, int G, int E,
+                                      int64_t T, int64_t N, int64_t K, hipStream_t stream);
+hipError_t launch_activation_backward(int act, const void* dc, const void* z, void* dz, int64_t T, int64_t N,
+                                      hipStream_t stream);
+
 // One wave: out[0] = shader-clock ticks, out[1] = 100 MHz ticks (>= ticks) of one sleep window.
 hipError_t launch_clock_probe(unsigned long long* out, unsigned long long ticks, hipStream_t stream);
 

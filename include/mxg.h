@@ -801,6 +801,155 @@ mxg_status mx_silu_backward_block128(const void* h_bf16, const void* dy_bf16, vo
                                      int64_t total_rows, int64_t I, hipStream_t stream);
 
 /*
+ * mx_rmsnorm -- the residual's addition, the root-mean-square norm and the 8-bit
+ * encoding of its output in one pass: what makes the router's and the experts'
+ * input.  mx_rmsnorm_backward -- its gradient.
+ * (NvMxf4f8Strategy, grouped_quantize(): the quantised operand's source; the pages
+ *  do not say how the tokens' rows are made.)
+ *
+ * Per row of H elements:
+ *   h = x + residual, rounded to stream_type;  without a residual h = x
+ *   r = 1 / sqrt(sum h^2 / H + eps)
+ *   y = h * r * (weight + weight_offset)
+ *
+ *   x         [num_tokens, H]: BF16 where residual is given, else of stream_type.
+ *   residual  [num_tokens, H] of stream_type, or NULL.
+ *   h         [num_tokens, H] of stream_type: the stream as it goes on; given exactly
+ *             where residual is, and may be residual itself (or x, in BF16).
+ *   weight    [H] of weight_type (MXG_F32 or MXG_BF16).
+ *   y_bf16    [num_tokens, H] or NULL.
+ *   q, scales with a format other than MXG_NORM_PLAIN, else NULL: the codes u8
+ *             [num_tokens, H] and the scales of
+ *     MXG_NORM_FP8_ROWWISE   fp32 [num_tokens], as mx_grouped_quantize's rowwise,
+ *     MXG_NORM_MXFP8         E8M0 u8 [num_tokens, H/32], as its MXFP8,
+ *     MXG_NORM_FP8_BLOCK128  fp32 [num_tokens, ceil(H/128)], as
+ *                            mx_grouped_quantize_block128,
+ *             of y in fp32 (no bf16 between).
+ * Sums and y are fp32; a row's squares are summed in a fixed order.  A row whose
+ * sum of squares passes fp32's range is treated as one with an infinity: r = 0.  A row
+ * or block with a NaN or infinity in y gets a non-finite scale (E8M0: 255) and in the
+ * fp32-scaled formats the codes of its quotients (as the block-128 quantisers), in
+ * MXFP8 NaN codes.
+ *
+ * Backward, with g = dy * (weight + weight_offset):
+ *   dx      = dh + r * g - h * r^3 * (sum g h) / H
+ *   dweight = sum over the rows of dy * h * r
+ *   dy_bf16   [num_tokens, H]: the gradient of y (of its codes too: the rounding
+ *             is passed through).
+ *   h         [num_tokens, H] of stream_type, as the forward wrote (or read) it.
+ *   dh        [num_tokens, H] of stream_type or NULL: what comes back to h past
+ *             the norm.
+ *   dx        [num_tokens, H] of stream_type, or NULL: the gradient of h, so of the
+ *             residual and of x; may be dh itself.
+ *   dx_bf16   [num_tokens, H] or NULL: the same rounded to BF16 (for x, where the
+ *             stream is fp32).
+ *   dweight   fp32 [H] or NULL, and with it
+ *   workspace fp32, mx_rmsnorm_workspace_bytes(num_tokens, H) bytes: the rows' sums
+ *             by workgroup, added in a fixed order.  Calls that may run at the same
+ *             time need workspaces of their own.
+ * At least one of dx, dx_bf16 and dweight is given.  num_tokens == 0 writes a
+ * dweight of zeros and nothing else.  Outputs may not overlap inputs or each other
+ * but as said.
+ *
+ * Errors: INVALID_VALUE for a bad type or format, H <= 0, num_tokens < 0, eps
+ * negative or NaN, a null pointer that has to be given or one given that may not be
+ * (h without residual, q with MXG_NORM_PLAIN, no output at all), or misalignment
+ * (rows, weight and codes on 16 bytes, the rest on 4); NOT_SUPPORTED for H % 8 != 0
+ * (with q: H % 32 != 0) or H or num_tokens > INT32_MAX / 2.
+ * mx_rmsnorm_workspace_bytes returns -1 for sizes that the call would refuse.
+ */
+typedef enum {
+    MXG_NORM_PLAIN = 0,
+    MXG_NORM_FP8_ROWWISE = 1,
+    MXG_NORM_MXFP8 = 2,
+    MXG_NORM_FP8_BLOCK128 = 3
+} mxg_norm_format;
+
+mxg_status mx_rmsnorm(mxg_norm_format format, mxg_dtype stream_type, const void* x, const void* residual,
+                      mxg_dtype weight_type, const void* weight, float weight_offset, float eps, int64_t num_tokens,
+                      int64_t H, void* h, void* y_bf16, void* q, void* scales, hipStream_t stream);
+int64_t mx_rmsnorm_workspace_bytes(int64_t num_tokens, int64_t H);
+mxg_status mx_rmsnorm_backward(mxg_dtype stream_type, const void* dy_bf16, const void* h, mxg_dtype weight_type,
+                               const void* weight, float weight_offset, float eps, const void* dh, int64_t num_tokens,
+                               int64_t H, void* dx, void* dx_bf16, float* dweight, float* workspace,
+                               hipStream_t stream);
+
+/*
+ * mx_grouped_matmul_bf16 -- ragged grouped product of BF16 operands with bias,
+ * activation and residual in its epilogue: the products around the experts that stay
+ * in BF16 (router logits, shared experts, projections) and experts trained in BF16.
+ * (grouped_matmul_rowwise_dynamic_scaled_fp8 without its scales; its
+ *  elementwise_lambda_fn is the place of the epilogue.)
+ *
+ * For each taken group g with e = expert_ids[g] and each row t it owns:
+ *   z[t,n] = sum_k a[t,k] b[e,n,k] + bias[e,n]
+ *   c[t,n] = act(z[t,n]) + residual[t,n]
+ * with act none, relu max(z, 0), gelu z (1 + erf(z / sqrt 2)) / 2, silu z / (1 + e^-z),
+ * or swiglu, which takes pairs of columns (2j = gate, 2j+1 = up, the layout of
+ * mx_silu_quantize): c[t,j] = silu(z[t,2j]) z[t,2j+1].
+ *
+ *   a_bf16  [total_rows, K]; b_bf16 [num_experts, N, K]; bias fp32 [num_experts, N]
+ *           or NULL.
+ *   residual, c  [total_rows, N] (swiglu: [total_rows, N/2]) of c_type; residual may
+ *           be NULL, or c itself.
+ *   z_bf16  [total_rows, N] or NULL: z rounded once, which the gradient takes.
+ *   row_offsets, expert_ids  as in mx_grouped_matmul; both NULL with num_groups =
+ *           num_experts = 1: one dense product over all rows.
+ * Sums and the epilogue are fp32, c is rounded once; act sees z in fp32, whether or not
+ * it is kept.  Only covered rows are written.  max_rows_per_group_hint as in
+ * mx_grouped_matmul.  Operands are not rounded; a call repeated gives the same bits.
+ *
+ * mx_grouped_matmul_bf16_backward -- the gradient of the rows, through the
+ * activation before them:
+ *   da[t,k] = act'(z[t,k]) * sum_n dc[t,n] b[e,n,k]
+ *   dc_bf16 [total_rows, N]; z_bf16 [total_rows, K], the pre-activations of the
+ *   product that made these rows; da_bf16 [total_rows, K], may be z itself.  swiglu:
+ *   z and da are [total_rows, 2K], columns 2j and 2j+1 from the k = j-th sum.  act none
+ *   takes no z.  relu' is 0 at 0.
+ * mx_grouped_matmul_bf16_backward_weights -- the gradient of b and bias:
+ *   dw[e,n,k] = sum over the rows t of the groups of expert e of dc[t,n] a[t,k]
+ *   dbias[e,n] = sum over those rows of dc[t,n]
+ *   dw [num_experts, N, K] of dw_type; dbias fp32 [num_experts, N] or NULL.  With
+ *   accumulate != 0 the sums are added to what dw and dbias hold, else they replace it
+ *   (zeros for an expert without rows).  Groups that name one expert are added in
+ *   their order.
+ * mx_activation_backward -- dz = act'(z) * dc by itself, for an activation no
+ *   product of the gradient follows: dc_bf16 [num_rows, N], z_bf16 and dz_bf16
+ *   [num_rows, N]; swiglu: z and dz [num_rows, 2N].  dz may be z or, without swiglu, dc.
+ * The residual's gradient is dc.  Outputs may not overlap inputs or each other but as
+ * said.
+ *
+ * Errors: INVALID_VALUE for a bad type or activation, N, K or num_experts <= 0,
+ * total_rows, num_rows or num_groups < 0, a null pointer that has to be given, z given
+ * to mx_grouped_matmul_bf16_backward with act none, mx_activation_backward with it, one
+ * of row_offsets and expert_ids without the other,
+ * NULL routing with num_groups or num_experts other than 1, or misalignment (16 bytes;
+ * bias, dbias, row_offsets and expert_ids 4); NOT_SUPPORTED for K % 8 != 0, in the
+ * gradients also N % 8 != 0, N odd with swiglu, K > MXG_MAX_K (the products' gradients: N
+ * too), N > INT32_MAX / 2, total_rows or num_rows > INT32_MAX, or num_groups >
+ * MXG_MAX_GROUPS.  total_rows or num_groups of 0 is a no-op, but for dw and dbias.
+ */
+typedef enum { MXG_ACT_NONE = 0, MXG_ACT_RELU = 1, MXG_ACT_GELU = 2, MXG_ACT_SILU = 3, MXG_ACT_SWIGLU = 4 } mxg_activation;
+
+mxg_status mx_grouped_matmul_bf16(mxg_activation act, const void* a_bf16, const void* b_bf16, const float* bias,
+                                  const void* residual, mxg_dtype c_type, void* c, void* z_bf16,
+                                  const uint32_t* row_offsets, const int32_t* expert_ids, int32_t num_groups,
+                                  int32_t num_experts, int64_t total_rows, int64_t N, int64_t K,
+                                  int64_t max_rows_per_group_hint, hipStream_t stream);
+mxg_status mx_grouped_matmul_bf16_backward(mxg_activation act, const void* dc_bf16, const void* b_bf16,
+                                           const void* z_bf16, void* da_bf16, const uint32_t* row_offsets,
+                                           const int32_t* expert_ids, int32_t num_groups, int32_t num_experts,
+                                           int64_t total_rows, int64_t N, int64_t K, int64_t max_rows_per_group_hint,
+                                           hipStream_t stream);
+mxg_status mx_grouped_matmul_bf16_backward_weights(const void* dc_bf16, const void* a_bf16, mxg_dtype dw_type,
+                                                   void* dw, float* dbias, int32_t accumulate,
+                                                   const uint32_t* row_offsets, const int32_t* expert_ids,
+                                                   int32_t num_groups, int32_t num_experts, int64_t total_rows,
+                                                   int64_t N, int64_t K, hipStream_t stream);
+mxg_status mx_activation_backward(mxg_activation act, const void* dc_bf16, const void* z_bf16, void* dz_bf16,
+                                  int64_t num_rows, int64_t N, hipStream_t stream);
+
+/*
  * mxg_clock_probe -- a measurement aid, not part of the path: one wave on
  * `stream` sleeps for window_us microseconds of the GPU's constant 100 MHz
  * counter and counts the shader clock meanwhile.  On completion
