@@ -102,7 +102,8 @@ mxg_status mx_grouped_matmul_bf16(mxg_activation act, const void* a_bf16, const 
         return MXG_ERROR_INVALID_VALUE;
     if (mxg_status st = check_groups(row_offsets, expert_ids, num_groups, num_experts, total_rows, stream)) return st;
     const mxg::Bf16Problem p{(int)act, a_bf16, b_bf16, bias, residual, c, c_type == MXG_F32, z_bf16, row_offsets,
-                             expert_ids, num_groups, num_experts, total_rows, N, K, max_rows_per_group_hint};
+                             expert_ids, num_groups, num_experts, total_rows, N, K, max_rows_per_group_hint,
+                             aligned(bias, 16)};
     return from_hip(mxg::launch_matmul_bf16(p, stream));
 }
 
@@ -123,7 +124,7 @@ mxg_status mx_grouped_matmul_bf16_backward(mxg_activation act, const void* dc_bf
     if (mxg_status st = check_groups(row_offsets, expert_ids, num_groups, num_experts, total_rows, stream)) return st;
     const mxg::Bf16Problem p{(int)act, dc_bf16, b_bf16, nullptr, nullptr, da_bf16, false, const_cast<void*>(z_bf16),
                              row_offsets, expert_ids, num_groups, num_experts, total_rows, N, K,
-                             max_rows_per_group_hint};
+                             max_rows_per_group_hint, false};
     return from_hip(mxg::launch_matmul_bf16_backward(p, stream));
 }
 

@@ -56,16 +56,17 @@ __device__ __forceinline__ void with_act(int act, F f) {
     }
 }
 
-// W neighbouring elements at p (fp32 or bf16): whole (aligned to W elements), or the first n.
+// W (4 or 8) neighbouring elements at p (fp32 or bf16): whole (aligned to W elements, fp32 to 4), or the first n.
 template <int W>
 __device__ __forceinline__ void load_n(const void* p, bool f32, bool whole, int n, float* v) {
     if (f32) {
         const float* q = static_cast<const float*>(p);
         if (whole) {
-            typedef float vt __attribute__((ext_vector_type(W)));
-            const vt x = *reinterpret_cast<const vt*>(q);
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = x[i];
+            for (int i = 0; i < W; i += 4) {
+                const v4f x = *reinterpret_cast<const v4f*>(q + i);
+                v[i] = x[0], v[i + 1] = x[1], v[i + 2] = x[2], v[i + 3] = x[3];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i) v[i] = i < n ? q[i] : 0.0f;
@@ -88,11 +89,8 @@ __device__ __forceinline__ void store_n(void* p, bool f32, bool whole, int n, co
     if (f32) {
         float* q = static_cast<float*>(p);
         if (whole) {
-            typedef float vt __attribute__((ext_vector_type(W)));
-            vt x;
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[i] = v[i];
-            *reinterpret_cast<vt*>(q) = x;
+            for (int i = 0; i < W; i += 4) *reinterpret_cast<v4f*>(q + i) = v4f{v[i], v[i + 1], v[i + 2], v[i + 3]};
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i)
@@ -113,78 +111,83 @@ __device__ __forceinline__ void store_n(void* p, bool f32, bool whole, int n, co
     }
 }
 
-// The forward epilogue of columns col .. col + 3 (those below N) of row t of expert e,
+// The forward epilogue of columns col .. col + 7 (those below N) of row t of expert e,
 // from the sums v.
 template <int ACT>
-__device__ __forceinline__ void finish4(const Bf16Problem& p, int e, int64_t t, int64_t col, const float* sums) {
-    const int n = (int)(p.N - col < 4 ? p.N - col : 4);
-    const bool whole = (p.N & 3) == 0;
-    float v[4];
+__device__ __forceinline__ void finish8(const Bf16Problem& p, int e, int64_t t, int64_t col, const float* sums) {
+    const int n = (int)(p.N - col < 8 ? p.N - col : 8);
+    const bool whole = (p.N & 7) == 0;
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = sums[i];
+    for (int i = 0; i < 8; ++i) v[i] = sums[i];
     if (p.bias) {
-        float b[4];
-        load_n<4>(p.bias + e * p.N + col, true, false, n, b);  // bias is aligned to its elements only
+        float b[8];
+        load_n<8>(p.bias + e * p.N + col, true, whole && p.bias16, n, b);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += b[i];
+        for (int i = 0; i < 8; ++i) v[i] += b[i];
     }
-    if (p.z) store_n<4>(static_cast<uint16_t*>(p.z) + t * p.N + col, false, whole, n, v);
+    if (p.z) store_n<8>(static_cast<uint16_t*>(p.z) + t * p.N + col, false, whole, n, v);
     const int size = p.c32 ? 4 : 2;
     if constexpr (ACT == kSwiglu) {
-        float y[2] = {activate<kSilu>(v[0]) * v[1], activate<kSilu>(v[2]) * v[3]};
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = activate<kSilu>(v[2 * i]) * v[2 * i + 1];
         const int64_t at = (t * (p.N / 2) + col / 2) * size;
         if (p.res) {
-            float r[2];
-            load_n<2>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n / 2, r);
-            y[0] += r[0];
-            y[1] += r[1];
+            float r[4];
+            load_n<4>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n / 2, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] += r[i];
         }
-        store_n<2>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n / 2, y);
+        store_n<4>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n / 2, y);
     } else {
         const int64_t at = (t * p.N + col) * size;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
         if (p.res) {
-            float r[4];
-            load_n<4>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n, r);
+            float r[8];
+            load_n<8>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n, r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += r[i];
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
         }
-        store_n<4>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n, v);
+        store_n<8>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n, v);
     }
 }
 
-// d times the derivative at z, eight columns (swiglu: of four sums).
-__device__ __forceinline__ void swiglu_grad4(const float* z, const float* d, float* out) {
+// d times the derivative at z: the gate and up columns of N sums.
+template <int N>
+__device__ __forceinline__ void swiglu_grad(const float* z, const float* d, float* out) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float g = z[2 * i], u = z[2 * i + 1], s = sigmoid(g);
         out[2 * i] = d[i] * u * s * (1.0f + g * (1.0f - s));
         out[2 * i + 1] = d[i] * g * s;
     }
 }
 
-// The backward epilogue of columns col .. col + 3 of row t (K is a multiple of 8: all of them).
+// The backward epilogue of columns col .. col + 7 of row t (K is a multiple of 8: all of them).
 template <int ACT>
-__device__ __forceinline__ void finish4_backward(const Bf16Problem& p, int64_t t, int64_t col, const float* d) {
+__device__ __forceinline__ void finish8_backward(const Bf16Problem& p, int64_t t, int64_t col, const float* d) {
     if constexpr (ACT == kSwiglu) {
         const int64_t at = (t * p.K + col) * 2;
-        float z[8], out[8];
+        float z[16], out[16];
         load_n<8>(static_cast<const uint16_t*>(p.z) + at, false, true, 8, z);
-        swiglu_grad4(z, d, out);
+        load_n<8>(static_cast<const uint16_t*>(p.z) + at + 8, false, true, 8, z + 8);
+        swiglu_grad<8>(z, d, out);
         store_n<8>(static_cast<uint16_t*>(p.c) + at, false, true, 8, out);
+        store_n<8>(static_cast<uint16_t*>(p.c) + at + 8, false, true, 8, out + 8);
     } else {
         const int64_t at = t * p.K + col;
-        float v[4];
+        float v[8];
         if constexpr (ACT == kNone) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = d[i];
+            for (int i = 0; i < 8; ++i) v[i] = d[i];
         } else {
-            load_n<4>(static_cast<const uint16_t*>(p.z) + at, false, true, 4, v);
+            load_n<8>(static_cast<const uint16_t*>(p.z) + at, false, true, 8, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = d[i] * derivative<ACT>(v[i]);
+            for (int i = 0; i < 8; ++i) v[i] = d[i] * derivative<ACT>(v[i]);
         }
-        store_n<4>(static_cast<uint16_t*>(p.c) + at, false, true, 4, v);
+        store_n<8>(static_cast<uint16_t*>(p.c) + at, false, true, 8, v);
     }
 }
 

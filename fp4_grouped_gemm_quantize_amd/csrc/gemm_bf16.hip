@@ -1,7 +1,9 @@
 // gemm_bf16.hip -- ragged grouped product of BF16 operands with bias, activation and
 // residual in its epilogue, the gradient of its rows through the activation before
 // them, and the activation's gradient by itself, for gfx950.
-#include "gemm_bf16.h"
+#include <stdlib.h>
+
+#include "gemm_bf16_tile.h"
 
 namespace mxg {
 
@@ -9,83 +11,146 @@ using namespace bf16;
 
 namespace {
 
-constexpr int kTile = 64, kDepth = 32, kPitch = kDepth + 8, kThreads = 256;
+// The tiles of a ragged product: BACK reads the weights wide (its depth is their row
+// index) and ends in the backward epilogue.
+template <class TL, bool BACK>
+struct RowsJob {
+    struct Coord {
+        int e, rows_in, cols_in;
+        int64_t m0, n0, stages, depth;
+        const uint8_t *a, *b;
+    };
+    const Bf16Problem& p;
+    const uint32_t* s_pre;  // M tiles before each group, then of all
+    const uint32_t* s_off;
+    const int32_t* s_ids;
+    int64_t ntn;
+    int mband;
+    gemm::WorkSplit ws;
+    int64_t lda, ldb, cols, deep, grid;
 
-// One 64 x 64 tile a workgroup: blockIdx.x the column tile, blockIdx.y the row tile
-// among all groups' (found by a walk over the groups).
-template <bool BACK>
-__global__ __launch_bounds__(kThreads) void matmul_bf16_kernel(const Bf16Problem p) {
-    __shared__ __attribute__((aligned(16))) uint16_t s_a[kTile * kPitch], s_b[kTile * kPitch];
-    const int64_t cols = BACK ? p.K : p.N, depth = BACK ? p.N : p.K;
-    int64_t left = blockIdx.y;
-    int g = 0;
-    GroupRange r{0, 0};
-    for (; g < p.G; ++g) {
-        r = rows_of(p.off, p.ids, g, p.T, p.E);
-        const int64_t tiles = (r.hi - r.lo + kTile - 1) / kTile;
-        if (left < tiles) break;
-        left -= tiles;
+    __device__ __forceinline__ bool next(int64_t& W, Coord& c) const {
+        for (; W < ws.items; W += grid) {
+            locate(W, c);
+            if (c.cols_in > 0) return true;  // the second half of a narrow last tile has no columns
+        }
+        return false;
     }
-    if (g == p.G) return;
-    const int e = expert_of(p.ids, g);
-    const int64_t m0 = r.lo + left * kTile, n0 = (int64_t)blockIdx.x * kTile;
-    const uint16_t* a = static_cast<const uint16_t*>(p.a);
-    const uint16_t* b = static_cast<const uint16_t*>(p.b) + (int64_t)e * p.N * p.K;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, wm = wave / 2, wn = wave % 2, l16 = lane & 15,
-              kg = lane >> 4;
-    v4f acc[2][2];
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int64_t k0 = 0; k0 < depth; k0 += kDepth) {
-        {
-            const int row = tid / 4, piece = tid % 4;
-            const int64_t k = k0 + piece * 8;
-            uint4 v = make_uint4(0, 0, 0, 0), w = v;
-            if (m0 + row < r.hi && k < depth) v = *reinterpret_cast<const uint4*>(a + (m0 + row) * depth + k);
-            *reinterpret_cast<uint4*>(s_a + row * kPitch + piece * 8) = v;
-            if constexpr (!BACK) {
-                if (n0 + row < cols && k < depth) w = *reinterpret_cast<const uint4*>(b + (n0 + row) * depth + k);
-                *reinterpret_cast<uint4*>(s_b + row * kPitch + piece * 8) = w;
-            } else {
-                const int kr = tid / 8, c8 = (tid % 8) * 8;
-                if (k0 + kr < depth && n0 + c8 < cols)
-                    w = *reinterpret_cast<const uint4*>(b + (k0 + kr) * cols + n0 + c8);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-                for (int i = 0; i < 8; ++i) s_b[(c8 + i) * kPitch + kr] = (uint16_t)(ww[i / 2] >> (16 * (i & 1)));
-            }
+    // The tile of item W: its group by a two-step search of the prefix (64 lanes over
+    // every 16th entry, then 16).  Tiles run in bands of mband M tiles, N outer in a band.
+    __device__ __forceinline__ void locate(int64_t W, Coord& c) const {
+        const bool split = W >= ws.full;
+        const int64_t L = split ? ws.full + (W - ws.full) / 2 : W;
+        const uint32_t x = (uint32_t)(L / ntn);
+        const int lane = fresh_lane(), l16 = lane & 15, G = p.G;
+        uint64_t m = __ballot(lane * 16 <= G && s_pre[lane * 16 <= G ? lane * 16 : 0] <= x);
+        const int base = (__popcll(m) - 1) * 16, idx = base + l16;
+        m = __ballot(lane < 16 && idx <= G && s_pre[idx <= G ? idx : 0] <= x);
+        const int g = base + __popcll(m) - 1;
+        const int first = (int)s_pre[g], mtiles = (int)s_pre[g + 1] - first;
+        const int64_t local = L - first * ntn;
+        const int mb = mband < mtiles ? mband : mtiles;
+        const int band = (int)(local / (mb * ntn));
+        const int64_t r = local - band * mb * ntn;
+        const int left = mtiles - band * mb, gm = left < mb ? left : mb;
+        const int64_t lo = (int64_t)s_off[g] < p.T ? (int64_t)s_off[g] : p.T;
+        const int64_t hi = (int64_t)s_off[g + 1] < p.T ? (int64_t)s_off[g + 1] : p.T;
+        c.e = __builtin_amdgcn_readfirstlane(s_ids[g]);
+        c.m0 = gemm::first_lane64(lo + (int64_t)(band * mb + (int)(r % gm)) * TL::BM);
+        c.rows_in = __builtin_amdgcn_readfirstlane((int)(hi - c.m0 < TL::BM ? hi - c.m0 : TL::BM));
+        int64_t n0 = r / gm * TL::BN;
+        int width = TL::BN;
+        if (split) {  // half a tile along N
+            width = TL::BN / 2;
+            if ((W - ws.full) % 2) n0 += TL::BN / 2;
         }
-        __syncthreads();
-        v8b fa[2], fb[2];
-        for (int i = 0; i < 2; ++i) {
-            fa[i] = *reinterpret_cast<const v8b*>(s_a + (wm * 32 + i * 16 + l16) * kPitch + kg * 8);
-            fb[i] = *reinterpret_cast<const v8b*>(s_b + (wn * 32 + i * 16 + l16) * kPitch + kg * 8);
-        }
-        for (int i = 0; i < 2; ++i)
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[i], fa[j], acc[i][j], 0, 0, 0);
-        __syncthreads();
+        c.n0 = gemm::first_lane64(n0);
+        const int64_t rest = cols - c.n0;
+        c.cols_in = __builtin_amdgcn_readfirstlane((int)(rest < width ? rest : width));
+        c.depth = deep;
+        c.stages = (deep + kStageDepth - 1) / kStageDepth;
+        c.a = static_cast<const uint8_t*>(p.a) + c.m0 * lda;
+        c.b = static_cast<const uint8_t*>(p.b) + (int64_t)c.e * p.N * p.K * 2 + c.n0 * (BACK ? 2 : ldb);
     }
-    with_act(p.act, [&](auto act) {
-        for (int j = 0; j < 2; ++j) {
-            const int64_t t = m0 + wm * 32 + j * 16 + l16;
-            if (t >= r.hi) continue;
-            for (int i = 0; i < 2; ++i) {
-                const int64_t col = n0 + wn * 32 + i * 16 + kg * 4;
-                if (col >= cols) continue;
-                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if constexpr (BACK) finish4_backward<act()>(p, t, col, v);
-                else finish4<act()>(p, e, t, col, v);
-            }
+    __device__ __forceinline__ bool segment(Coord&) const { return false; }
+
+    template <class>
+    __device__ __forceinline__ void finish(const Coord& c, const v4f (&acc)[TL::TN][TL::TM], int wm, int wn,
+                                           uint8_t* out) const {
+        with_act(p.act, [&](auto act) {
+            put_blocks<TL>(acc, wm, wn, out, [&](int row, int col, const float* v) {
+                if (row >= c.rows_in || col >= c.cols_in) return;
+                if constexpr (BACK) finish8_backward<act()>(p, c.m0 + row, c.n0 + col, v);
+                else finish8<act()>(p, c.e, c.m0 + row, c.n0 + col, v);
+            });
+        });
+    }
+};
+
+template <class TL, bool BACK>
+__global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16Problem p, int64_t ntn, int mband) {
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring[TL::kLds];
+    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
+    __shared__ int32_t s_ids[kMaxGroups];
+    const int tid = threadIdx.x, G = p.G;
+    for (int i = tid; i <= G; i += TL::kThreads) {
+        s_off[i] = p.off ? p.off[i] : i ? (uint32_t)p.T : 0;
+        if (i < G) s_ids[i] = p.ids ? p.ids[i] : 0;
+    }
+    __syncthreads();
+    // M tiles before each group
+    constexpr int kPer = (kMaxGroups + TL::kThreads - 1) / TL::kThreads;
+    uint32_t cnt[kPer], local = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int g = tid * kPer + i;
+        cnt[i] = 0;
+        if (g < G) {
+            const GroupRange r = group_range(s_off, s_ids, g, p.T, p.E);
+            cnt[i] = (uint32_t)((r.hi - r.lo + TL::BM - 1) / TL::BM);
         }
-    });
+        local += cnt[i];
+    }
+    uint32_t before = gemm::block_exclusive_scan<TL::kThreads>(local, s_wave, &total);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int g = tid * kPer + i;
+        if (g < G) s_pre[g] = before;
+        before += cnt[i];
+    }
+    if (tid == 0) s_pre[G] = total;
+    __syncthreads();
+    const int64_t cols = BACK ? p.K : p.N, deep = BACK ? p.N : p.K;
+    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, gemm::work_split((int64_t)total * ntn, gridDim.x),
+                          deep * 2, BACK ? cols * 2 : deep * 2, cols, deep, gridDim.x};
+    run_tiles<TL>(job, s_ring, gemm::xcd_remap(blockIdx.x, gridDim.x), gridDim.x);
+}
+
+int64_t compute_units() {
+    const int cus = gemm::device_cus();
+    return cus > 0 ? cus : 256;
+}
+
+template <class TL, bool BACK>
+hipError_t launch_tile(const Bf16Problem& p, int per_cu, int mband, hipStream_t stream) {
+    const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
+    const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
+    const int64_t room = compute_units() * per_cu, grid = most < room ? most : room;
+    hipLaunchKernelGGL((matmul_bf16_kernel<TL, BACK>), dim3((unsigned)grid), dim3(TL::kThreads), 0, stream, p, ntn,
+                       mband);
+    return hipGetLastError();
 }
 
 template <bool BACK>
 hipError_t launch(const Bf16Problem& p, hipStream_t stream) {
-    const int64_t cols = BACK ? p.K : p.N;
-    const dim3 grid((unsigned)((cols + kTile - 1) / kTile), (unsigned)(p.T / kTile + p.G));
-    hipLaunchKernelGGL(matmul_bf16_kernel<BACK>, grid, dim3(kThreads), 0, stream, p);
-    return hipGetLastError();
+    using Large = Tile<256, 256, 4, 2, false, BACK>;
+    using Mid = Tile<128, 128, 2, 2, false, BACK>;
+    using Small = Tile<32, 128, 1, 4, false, BACK>;
+    const char* f = getenv("MXG_BF16_TILE");
+    const int t = f ? atoi(f) : 256;
+    if (t == 128) return launch_tile<Mid, BACK>(p, 2, 4, stream);
+    if (t == 32) return launch_tile<Small, BACK>(p, 3, 1 << 30, stream);
+    return launch_tile<Large, BACK>(p, 1, 4, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -99,7 +164,7 @@ __global__ __launch_bounds__(256) void activation_backward_kernel(const void* dc
         if constexpr (ACT == kSwiglu) {
             float d[4];
             load_n<4>(static_cast<const uint16_t*>(dc) + u * 4, false, true, 4, d);
-            swiglu_grad4(zv, d, out);
+            swiglu_grad<4>(zv, d, out);
         } else {
             load_n<8>(static_cast<const uint16_t*>(dc) + u * 8, false, true, 8, out);
 #pragma unroll

@@ -144,6 +144,7 @@ struct Bf16Problem {
     int64_t N;
     int64_t K;
     int64_t max_rows_hint;
+    bool bias16;        // bias lies on 16 bytes
 };
 hipError_t launch_matmul_bf16(const Bf16Problem& p, hipStream_t stream);
 hipError_t launch_matmul_bf16_backward(const Bf16Problem& p, hipStream_t stream);
