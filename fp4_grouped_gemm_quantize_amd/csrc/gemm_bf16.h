@@ -111,10 +111,23 @@ __device__ __forceinline__ void store_n(void* p, bool f32, bool whole, int n, co
     }
 }
 
-// The forward epilogue of columns col .. col + 7 (those below N) of row t of expert e,
-// from the sums v.
+// The forward epilogue of columns col .. col + 7 (those below N) of row t of expert e, from
+// the sums v: the residual, asked for ahead, and the rest.
+struct Beside {
+    float res[8];
+};
 template <int ACT>
-__device__ __forceinline__ void finish8(const Bf16Problem& p, int e, int64_t t, int64_t col, const float* sums) {
+__device__ __forceinline__ void fetch8(const Bf16Problem& p, int64_t t, int64_t col, Beside& x) {
+    if (!p.res) return;
+    const int n = (int)(p.N - col < 8 ? p.N - col : 8), size = p.c32 ? 4 : 2;
+    const bool whole = (p.N & 7) == 0;
+    if constexpr (ACT == kSwiglu)
+        load_n<4>(static_cast<const uint8_t*>(p.res) + (t * (p.N / 2) + col / 2) * size, p.c32, whole, n / 2, x.res);
+    else load_n<8>(static_cast<const uint8_t*>(p.res) + (t * p.N + col) * size, p.c32, whole, n, x.res);
+}
+template <int ACT>
+__device__ __forceinline__ void finish8(const Bf16Problem& p, int e, int64_t t, int64_t col, const float* sums,
+                                        const Beside& x) {
     const int n = (int)(p.N - col < 8 ? p.N - col : 8);
     const bool whole = (p.N & 7) == 0;
     float v[8];
@@ -131,26 +144,18 @@ __device__ __forceinline__ void finish8(const Bf16Problem& p, int e, int64_t t, 
     if constexpr (ACT == kSwiglu) {
         float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = activate<kSilu>(v[2 * i]) * v[2 * i + 1];
-        const int64_t at = (t * (p.N / 2) + col / 2) * size;
-        if (p.res) {
-            float r[4];
-            load_n<4>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n / 2, r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] += r[i];
+        for (int i = 0; i < 4; ++i) {
+            y[i] = activate<kSilu>(v[2 * i]) * v[2 * i + 1];
+            if (p.res) y[i] += x.res[i];
         }
-        store_n<4>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n / 2, y);
+        store_n<4>(static_cast<uint8_t*>(p.c) + (t * (p.N / 2) + col / 2) * size, p.c32, whole, n / 2, y);
     } else {
-        const int64_t at = (t * p.N + col) * size;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
-        if (p.res) {
-            float r[8];
-            load_n<8>(static_cast<const uint8_t*>(p.res) + at, p.c32, whole, n, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        for (int i = 0; i < 8; ++i) {
+            v[i] = activate<ACT>(v[i]);
+            if (p.res) v[i] += x.res[i];
         }
-        store_n<8>(static_cast<uint8_t*>(p.c) + at, p.c32, whole, n, v);
+        store_n<8>(static_cast<uint8_t*>(p.c) + (t * p.N + col) * size, p.c32, whole, n, v);
     }
 }
 
@@ -165,29 +170,38 @@ __device__ __forceinline__ void swiglu_grad(const float* z, const float* d, floa
     }
 }
 
-// The backward epilogue of columns col .. col + 7 of row t (K is a multiple of 8: all of them).
+// The backward epilogue of columns col .. col + 7 of row t (K is a multiple of 8: all of them):
+// the pre-activations, asked for ahead, and the rest.
+struct Before {
+    uint4 z[2];
+};
 template <int ACT>
-__device__ __forceinline__ void finish8_backward(const Bf16Problem& p, int64_t t, int64_t col, const float* d) {
+__device__ __forceinline__ void fetch8_backward(const Bf16Problem& p, int64_t t, int64_t col, Before& x) {
+    if constexpr (ACT == kSwiglu) {
+        const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + (t * p.K + col) * 2);
+        x.z[0] = at[0];
+        x.z[1] = at[1];
+    } else if constexpr (ACT != kNone) {
+        x.z[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + t * p.K + col);
+    }
+}
+template <int ACT>
+__device__ __forceinline__ void finish8_backward(const Bf16Problem& p, int64_t t, int64_t col, const float* d,
+                                                 const Before& x) {
     if constexpr (ACT == kSwiglu) {
         const int64_t at = (t * p.K + col) * 2;
         float z[16], out[16];
-        load_n<8>(static_cast<const uint16_t*>(p.z) + at, false, true, 8, z);
-        load_n<8>(static_cast<const uint16_t*>(p.z) + at + 8, false, true, 8, z + 8);
+        unpack8(x.z[0], z);
+        unpack8(x.z[1], z + 8);
         swiglu_grad<8>(z, d, out);
         store_n<8>(static_cast<uint16_t*>(p.c) + at, false, true, 8, out);
         store_n<8>(static_cast<uint16_t*>(p.c) + at + 8, false, true, 8, out + 8);
     } else {
-        const int64_t at = t * p.K + col;
         float v[8];
-        if constexpr (ACT == kNone) {
+        if constexpr (ACT != kNone) unpack8(x.z[0], v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = d[i];
-        } else {
-            load_n<8>(static_cast<const uint16_t*>(p.z) + at, false, true, 8, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = d[i] * derivative<ACT>(v[i]);
-        }
-        store_n<8>(static_cast<uint16_t*>(p.c) + at, false, true, 8, v);
+        for (int i = 0; i < 8; ++i) v[i] = ACT == kNone ? d[i] : d[i] * derivative<ACT>(v[i]);
+        store_n<8>(static_cast<uint16_t*>(p.c) + t * p.K + col, false, true, 8, v);
     }
 }
 

@@ -16,21 +16,20 @@ namespace {
 template <class TL, bool BACK>
 struct RowsJob {
     struct Coord {
-        int e, rows_in, cols_in;
-        int64_t m0, n0, stages, depth;
+        int e, rows_in, cols_in, m0, n0, stages, depth;
         const uint8_t *a, *b;
     };
     const Bf16Problem& p;
     const uint32_t* s_pre;  // M tiles before each group, then of all
     const uint32_t* s_off;
     const int32_t* s_ids;
-    int64_t ntn;
-    int mband;
-    gemm::WorkSplit ws;
-    int64_t lda, ldb, cols, deep, grid;
+    int ntn, mband;
+    Items items;
+    int64_t lda, ldb;
+    int cols, deep, grid;
 
-    __device__ __forceinline__ bool next(int64_t& W, Coord& c) const {
-        for (; W < ws.items; W += grid) {
+    __device__ __forceinline__ bool next(int& W, Coord& c) const {
+        for (; W < items.all; W += grid) {
             locate(W, c);
             if (c.cols_in > 0) return true;  // the second half of a narrow last tile has no columns
         }
@@ -38,35 +37,31 @@ struct RowsJob {
     }
     // The tile of item W: its group by a two-step search of the prefix (64 lanes over
     // every 16th entry, then 16).  Tiles run in bands of mband M tiles, N outer in a band.
-    __device__ __forceinline__ void locate(int64_t W, Coord& c) const {
-        const bool split = W >= ws.full;
-        const int64_t L = split ? ws.full + (W - ws.full) / 2 : W;
-        const uint32_t x = (uint32_t)(L / ntn);
+    __device__ __forceinline__ void locate(int W, Coord& c) const {
+        const bool split = W >= items.full;
+        const int L = split ? items.full + (W - items.full) / 2 : W;
+        const uint32_t x = (uint32_t)L / (uint32_t)ntn;
         const int lane = fresh_lane(), l16 = lane & 15, G = p.G;
         uint64_t m = __ballot(lane * 16 <= G && s_pre[lane * 16 <= G ? lane * 16 : 0] <= x);
         const int base = (__popcll(m) - 1) * 16, idx = base + l16;
         m = __ballot(lane < 16 && idx <= G && s_pre[idx <= G ? idx : 0] <= x);
         const int g = base + __popcll(m) - 1;
         const int first = (int)s_pre[g], mtiles = (int)s_pre[g + 1] - first;
-        const int64_t local = L - first * ntn;
+        const uint32_t local = (uint32_t)(L - first * ntn);
         const int mb = mband < mtiles ? mband : mtiles;
-        const int band = (int)(local / (mb * ntn));
-        const int64_t r = local - band * mb * ntn;
+        const int band = (int)(local / (uint32_t)(mb * ntn));
+        const uint32_t r = local - (uint32_t)(band * mb * ntn);
         const int left = mtiles - band * mb, gm = left < mb ? left : mb;
+        const int nt = (int)(r / (uint32_t)gm), mt = band * mb + (int)r - nt * gm;
         const int64_t lo = (int64_t)s_off[g] < p.T ? (int64_t)s_off[g] : p.T;
         const int64_t hi = (int64_t)s_off[g + 1] < p.T ? (int64_t)s_off[g + 1] : p.T;
         c.e = __builtin_amdgcn_readfirstlane(s_ids[g]);
-        c.m0 = gemm::first_lane64(lo + (int64_t)(band * mb + (int)(r % gm)) * TL::BM);
-        c.rows_in = __builtin_amdgcn_readfirstlane((int)(hi - c.m0 < TL::BM ? hi - c.m0 : TL::BM));
-        int64_t n0 = r / gm * TL::BN;
-        int width = TL::BN;
-        if (split) {  // half a tile along N
-            width = TL::BN / 2;
-            if ((W - ws.full) % 2) n0 += TL::BN / 2;
-        }
-        c.n0 = gemm::first_lane64(n0);
-        const int64_t rest = cols - c.n0;
-        c.cols_in = __builtin_amdgcn_readfirstlane((int)(rest < width ? rest : width));
+        c.m0 = __builtin_amdgcn_readfirstlane((int)lo + mt * TL::BM);
+        const int rows = (int)hi - c.m0;
+        c.rows_in = __builtin_amdgcn_readfirstlane(rows < TL::BM ? rows : TL::BM);
+        const int width = split ? TL::BN / 2 : TL::BN;  // half a tile along N
+        c.n0 = __builtin_amdgcn_readfirstlane(nt * TL::BN + (split && (W - items.full) % 2 ? TL::BN / 2 : 0));
+        c.cols_in = cols - c.n0 < width ? cols - c.n0 : width;
         c.depth = deep;
         c.stages = (deep + kStageDepth - 1) / kStageDepth;
         c.a = static_cast<const uint8_t*>(p.a) + c.m0 * lda;
@@ -78,18 +73,32 @@ struct RowsJob {
     __device__ __forceinline__ void finish(const Coord& c, const v4f (&acc)[TL::TN][TL::TM], int wm, int wn,
                                            uint8_t* out) const {
         with_act(p.act, [&](auto act) {
-            put_blocks<TL>(acc, wm, wn, out, [&](int row, int col, const float* v) {
-                if (row >= c.rows_in || col >= c.cols_in) return;
-                if constexpr (BACK) finish8_backward<act()>(p, c.m0 + row, c.n0 + col, v);
-                else finish8<act()>(p, c.e, c.m0 + row, c.n0 + col, v);
-            });
+            if constexpr (BACK)
+                put_blocks<TL, Before>(
+                    acc, wm, wn, out,
+                    [&](int row, int col, Before& x) {
+                        if (row < c.rows_in && col < c.cols_in) fetch8_backward<act()>(p, c.m0 + row, c.n0 + col, x);
+                    },
+                    [&](int row, int col, const float* v, const Before& x) {
+                        if (row < c.rows_in && col < c.cols_in)
+                            finish8_backward<act()>(p, c.m0 + row, c.n0 + col, v, x);
+                    });
+            else
+                put_blocks<TL, Beside>(
+                    acc, wm, wn, out,
+                    [&](int row, int col, Beside& x) {
+                        if (row < c.rows_in && col < c.cols_in) fetch8<act()>(p, c.m0 + row, c.n0 + col, x);
+                    },
+                    [&](int row, int col, const float* v, const Beside& x) {
+                        if (row < c.rows_in && col < c.cols_in) finish8<act()>(p, c.e, c.m0 + row, c.n0 + col, v, x);
+                    });
         });
     }
 };
 
 template <class TL, bool BACK>
-__global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16Problem p, int64_t ntn, int mband) {
-    __shared__ __attribute__((aligned(16))) uint8_t s_ring[TL::kLds];
+__global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16Problem p, int ntn, int mband) {
+    __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
     __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
     __shared__ int32_t s_ids[kMaxGroups];
     const int tid = threadIdx.x, G = p.G;
@@ -120,10 +129,10 @@ __global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16
     }
     if (tid == 0) s_pre[G] = total;
     __syncthreads();
-    const int64_t cols = BACK ? p.K : p.N, deep = BACK ? p.N : p.K;
-    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, gemm::work_split((int64_t)total * ntn, gridDim.x),
-                          deep * 2, BACK ? cols * 2 : deep * 2, cols, deep, gridDim.x};
-    run_tiles<TL>(job, s_ring, gemm::xcd_remap(blockIdx.x, gridDim.x), gridDim.x);
+    const int cols = (int)(BACK ? p.K : p.N), deep = (int)(BACK ? p.N : p.K), grid = (int)gridDim.x;
+    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, items_of((int)total * ntn, grid),
+                          (int64_t)deep * 2, (int64_t)(BACK ? cols : deep) * 2, cols, deep, grid};
+    run_tiles<TL>(job, s_ring, gemm::xcd_remap((int)blockIdx.x, grid), grid);
 }
 
 int64_t compute_units() {
@@ -135,9 +144,10 @@ template <class TL, bool BACK>
 hipError_t launch_tile(const Bf16Problem& p, int per_cu, int mband, hipStream_t stream) {
     const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
     const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
+    if (2 * most > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
     const int64_t room = compute_units() * per_cu, grid = most < room ? most : room;
-    hipLaunchKernelGGL((matmul_bf16_kernel<TL, BACK>), dim3((unsigned)grid), dim3(TL::kThreads), 0, stream, p, ntn,
-                       mband);
+    hipLaunchKernelGGL((matmul_bf16_kernel<TL, BACK>), dim3((unsigned)grid), dim3(TL::kThreads), 0, stream, p,
+                       (int)ntn, mband);
     return hipGetLastError();
 }
 

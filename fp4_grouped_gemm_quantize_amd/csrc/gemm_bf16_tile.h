@@ -68,6 +68,7 @@ struct Operand {
         else return (row >> 3) & 1;
     }
 
+    static constexpr bool kWide = WIDE;
     uint32_t off[kLoads];
 
     static __device__ __forceinline__ int stage_row(int wave, int lane, int j) {
@@ -79,7 +80,7 @@ struct Operand {
         else return swz_chunk<128>(row, lane % 8);
     }
     // Offsets of a stage at whose base `real` rows (columns) and `depth` deep are left; ld: bytes a source row.
-    __device__ __forceinline__ void set(int wave, int lane, int real, int64_t depth, uint32_t ld) {
+    __device__ __forceinline__ void set(int wave, int lane, int real, int depth, uint32_t ld) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int row = stage_row(wave, lane, j), p = piece(row, lane);
@@ -90,34 +91,32 @@ struct Operand {
     // bytes the base moves a stage
     static __device__ __forceinline__ int64_t step(int64_t ld) { return WIDE ? kStageDepth * ld : 128; }
 
-    // This lane's part of a fragment's address: rows first .. first + 15 of the output side start
-    // at multiples of 16.
-    static __device__ __forceinline__ uint32_t lane_base(int lane) {
+    // This lane's part of the addresses of the fragments from the first-th on (of 16 rows each; first a
+    // multiple of how many there are).
+    static __device__ __forceinline__ uint32_t lane_base(int lane, int first) {
         const int l16 = lane & 15, kg = lane >> 4;
         if constexpr (WIDE) {
             const int row = kg * 8 + l16 / 4;
-            return row * kRowBytes + (turn(row) << 5) + (l16 & 3) * 8;
+            return row * kRowBytes + ((turn(row) ^ first) << 5) + (l16 & 3) * 8;
         } else {
-            return l16 * 128 + (swz_chunk<128>(l16, kg) << 4);
+            return (first * 16 + l16) * 128 + (swz_chunk<128>(l16, kg) << 4);
         }
     }
-    // Fragment of rows 16 f .. 16 f + 15, step (0 or 1), from the stage at `slot`.
-    static __device__ __forceinline__ v8b frag(const uint8_t* slot, uint32_t base, int f, int step) {
+    // The f-th of them, step (0 or 1); at: lane_base and the stage's LDS address, whose low 9 bits are 0.
+    static __device__ __forceinline__ v8b frag(uint32_t at, int f, int step) {
         if constexpr (WIDE) {
-            const uint8_t* p = slot + (base ^ (f << 5)) + step * 32 * kRowBytes;
             typedef v4s __attribute__((address_space(3)))* lp;
-            typedef uint8_t __attribute__((address_space(3)))* lb;
-            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)((lb)p));
-            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)((lb)p + 4 * kRowBytes));
+            const uint32_t p = (at ^ (f << 5)) + step * 32 * kRowBytes;
             union {
                 v4s s[2];
                 v8b b;
             } u;
-            u.s[0] = lo;
-            u.s[1] = hi;
+            u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(size_t)p);
+            u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(size_t)(p + 4 * kRowBytes));
             return u.b;
         } else {
-            return *reinterpret_cast<const v8b*>(slot + (base ^ (step << 6)) + f * (16 * 128));
+            typedef const v8b __attribute__((address_space(3)))* lp;
+            return *(lp)(size_t)((at ^ (step << 6)) + f * (16 * 128));
         }
     }
 };
@@ -142,6 +141,16 @@ struct Tile {
     static constexpr int loads_before(int i) { return kLoads * (i - kRead) / (TN - kRead); }
 };
 
+// Work items of a persistent launch of `grid` workgroups: whole tiles, but where the last round is at
+// most half full, each of its tiles is two items of half its columns.
+struct Items {
+    int full, all;  // items that are whole tiles; all of them
+};
+__device__ __forceinline__ Items items_of(int tiles, int grid) {
+    const int rest = tiles % grid;
+    return rest > 0 && 2 * rest <= grid ? Items{tiles - rest, tiles + rest} : Items{tiles, tiles};
+}
+
 // The lane number, made anew where it is needed: what derives from it holds no register
 // between stages.
 __device__ __forceinline__ int fresh_lane() {
@@ -151,14 +160,14 @@ __device__ __forceinline__ int fresh_lane() {
 }
 
 // Runs the tiles of `job`.  Job:
-//   Coord        int rows_in, cols_in; int64_t stages (of the whole tile), depth (of the present
-//                segment); const uint8_t *a, *b (that segment's first stage)
-//   bool next(int64_t& W, Coord&)   the first item from W on that there is, or false
+//   Coord        int rows_in, cols_in, stages (of the whole tile), depth (of the present segment);
+//                const uint8_t *a, *b (that segment's first stage)
+//   bool next(int& W, Coord&)       the first item from W on that there is, or false
 //   bool segment(Coord&)            the tile's next stretch of depth, or false
 //   lda, ldb                        bytes a row of the operands
-//   void finish(c, acc, wave, lane, out)   epilogue of a wave's accumulators
+//   void finish(c, acc, wm, wn, out)   epilogue of a wave's accumulators
 template <class TL, class Job>
-__device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t first, int64_t step) {
+__device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, int step) {
     constexpr int TM = TL::TM, TN = TL::TN;
     using A = typename TL::A;
     using B = typename TL::B;
@@ -166,14 +175,14 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t fir
     const int wm = wave / TL::WGN, wn = wave % TL::WGN;
 
     typename Job::Coord cc{};
-    int64_t cw = first;
+    int cw = first;
     if (!job.next(cw, cc)) return;  // workgroup-uniform
 
     // ---- the producer: two stages ahead.  Pointers, offsets and `left` (depth from its stage to
     // the segment's end) are those of its next stage; past the last tile every lane asks for
     // nothing, so that its loads need no branch.
     typename Job::Coord pc = cc;
-    int64_t pw = cw, left = 0;
+    int pw = cw, left = 0;
     uint64_t pa = 0, pb = 0;
     uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * 1024);
     const uint32_t slots = 2 * slot + TL::kStage;  // slot + the other slot
@@ -188,7 +197,7 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t fir
     auto begin = [&]() {  // the first stage of pc's segment
         pa = (uint64_t)gemm::first_lane64((int64_t)pc.a);
         pb = (uint64_t)gemm::first_lane64((int64_t)pc.b);
-        left = gemm::first_lane64(pc.depth);
+        left = __builtin_amdgcn_readfirstlane(pc.depth);
         offsets();
     };
     auto next_tile = [&](bool more) {
@@ -198,18 +207,30 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t fir
         }
         if (more) return begin();
         pc.rows_in = pc.cols_in = 0;
-        left = (int64_t)1 << 62;
+        left = 1 << 30;
         offsets();
     };
-    auto load = [&](int l) {
-        const v4i da = {(int)(uint32_t)pa, (int)(uint32_t)(pa >> 32), (int)kNowhere, 0x00020000};
-        const v4i db = {(int)(uint32_t)pb, (int)(uint32_t)(pb >> 32), (int)kNowhere, 0x00020000};
-        if (l < A::kLoads) lds_load(da, fa.off[l < A::kLoads ? l : 0], slot + l * (TL::kWaves * 1024));
-        else lds_load(db, fb.off[l < A::kLoads ? 0 : l - A::kLoads], slot + l * (TL::kWaves * 1024));
+    struct Where {
+        v4i da, db;
+        uint32_t slot;
+    };
+    auto where = [&]() {
+        // (scalar already; the lane reads say so where the compiler cannot tell)
+        const uint64_t ua = (uint64_t)gemm::first_lane64((int64_t)pa), ub = (uint64_t)gemm::first_lane64((int64_t)pb);
+        const Where w = {{(int)(uint32_t)ua, (int)(uint32_t)(ua >> 32), (int)kNowhere, 0x00020000},
+                         {(int)(uint32_t)ub, (int)(uint32_t)(ub >> 32), (int)kNowhere, 0x00020000},
+                         (uint32_t)__builtin_amdgcn_readfirstlane(slot)};
+        __asm__ volatile("s_nop 4");  // wait states of what a lane read wrote
+        return w;
+    };
+    auto load = [&](const Where& w, int l) {
+        if (l < A::kLoads) lds_load(w.da, fa.off[l < A::kLoads ? l : 0], w.slot + l * (TL::kWaves * 1024));
+        else lds_load(w.db, fb.off[l < A::kLoads ? 0 : l - A::kLoads], w.slot + l * (TL::kWaves * 1024));
     };
     auto load_all = [&]() {
+        const Where w = where();
 #pragma unroll
-        for (int l = 0; l < TL::kLoads; ++l) load(l);
+        for (int l = 0; l < TL::kLoads; ++l) load(w, l);
     };
     auto advance = [&]() {  // behind a stage's loads
         slot = slots - slot;
@@ -237,47 +258,50 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t fir
     uint32_t abase, bbase;
     {
         const int lane = threadIdx.x & (kWave - 1);
-        abase = A::lane_base(lane);
-        bbase = B::lane_base(lane);
+        abase = A::lane_base(lane, wm * TM);
+        bbase = B::lane_base(lane, wn * TN);
     }
-    const int a0 = wm * TM, b0 = wn * TN;  // the wave's first fragments
-    int cslot = 0;
-    auto first_frags = [&](const uint8_t* at) {
+    // this lane's addresses in the present stage and in the next (a wide operand's opaque, so that its
+    // fragments' own addresses are made where they are read and hold no registers)
+    uint32_t ca = gemm::lds_addr(s_ring) + abase, cb = gemm::lds_addr(s_ring) + A::kBytes + bbase;
+    const uint32_t turn_a = 2 * ca + TL::kStage, turn_b = 2 * cb + TL::kStage;
+    auto first_frags = [&]() {
 #pragma unroll
-        for (int i = 0; i < TN; ++i) nf[i] = B::frag(at + A::kBytes, bbase, b0 + i, 0);
+        for (int i = 0; i < TN; ++i) nf[i] = B::frag(cb, i, 0);
 #pragma unroll
-        for (int j = 0; j < TM; ++j) tf[0][j] = A::frag(at, abase, a0 + j, 0);
+        for (int j = 0; j < TM; ++j) tf[0][j] = A::frag(ca, j, 0);
     };
-    first_frags(s_ring);
-    bool drain = false;  // an epilogue's stores are outstanding: counted waits do not hold
+    bool ahead = false;  // the next stage has landed already
     for (;;) {
-        const bool live = a0 * 16 < cc.rows_in && b0 * 16 < cc.cols_in;  // wave-uniform
+        const bool live = wm * TM * 16 < cc.rows_in && wn * TN * 16 < cc.cols_in;  // wave-uniform
         v4f acc[TN][TM];
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        const int64_t stages = cc.stages;
+        const int stages = __builtin_amdgcn_readfirstlane(cc.stages);
         auto read_barrier = [&]() {
-            if (drain) gemm::wait_vmem<0>();
-            drain = false;
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's fragments are in registers
             __asm__ volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             __asm__ volatile("" ::: "memory");
         };
         if (live) {
-            for (int64_t kt = 0; kt < stages; ++kt) {
-                const uint8_t *cur = s_ring + cslot * TL::kStage, *nxt = s_ring + (cslot ^ 1) * TL::kStage;
+            first_frags();  // (read at the end of the tile before, too: they hold no registers through its epilogue)
+            for (int kt = 0; kt < stages; ++kt) {
+                const Where w = where();
+                uint32_t na = turn_a - ca, nb = turn_b - cb;
+                if constexpr (A::kWide) __asm__ volatile("" : "+v"(ca), "+v"(na));
+                if constexpr (B::kWide) __asm__ volatile("" : "+v"(cb), "+v"(nb));
 #pragma unroll
                 for (int i = 0; i < TN; ++i) {
 #pragma unroll
                     for (int j = 0; j < TM; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[i], tf[0][j], acc[i][j], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    nf[i] = B::frag(cur + A::kBytes, bbase, b0 + i, 1);
+                    nf[i] = B::frag(cb, i, 1);
 #pragma unroll
-                    for (int j = i * TM / TN; j < (i + 1) * TM / TN; ++j) tf[1][j] = A::frag(cur, abase, a0 + j, 1);
+                    for (int j = i * TM / TN; j < (i + 1) * TM / TN; ++j) tf[1][j] = A::frag(ca, j, 1);
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
@@ -289,33 +313,40 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t fir
                     if (i == TL::kRead) read_barrier();
                     if (i >= TL::kRead)
 #pragma unroll
-                        for (int q = TL::loads_before(i); q < TL::loads_before(i + 1); ++q) load(q);
+                        for (int q = TL::loads_before(i); q < TL::loads_before(i + 1); ++q) load(w, q);
                     if (i == TL::kLanded) {
-                        stage_barrier<TL::loads_before(TL::kLanded + 1)>();
-                        nf[0] = B::frag(nxt + A::kBytes, bbase, b0, 0);
+                        if (!ahead) gemm::wait_vmem<TL::loads_before(TL::kLanded + 1)>();
+                        ahead = false;
+                        read_barrier();
+                        nf[0] = B::frag(nb, 0, 0);
 #pragma unroll
-                        for (int j = 0; j < TM; ++j) tf[0][j] = A::frag(nxt, abase, a0 + j, 0);
+                        for (int j = 0; j < TM; ++j) tf[0][j] = A::frag(na, j, 0);
 #pragma unroll
-                        for (int f = 1; f <= i; ++f) nf[f] = B::frag(nxt + A::kBytes, bbase, b0 + f, 0);
+                        for (int f = 1; f <= i; ++f) nf[f] = B::frag(nb, f, 0);
                     }
-                    if (i > TL::kLanded) nf[i] = B::frag(nxt + A::kBytes, bbase, b0 + i, 0);
+                    if (i > TL::kLanded) nf[i] = B::frag(nb, i, 0);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 advance();
-                cslot ^= 1;
+                ca = na;
+                cb = nb;
             }
+            // The next tile's second stage is awaited here, before the epilogue's stores: behind them its
+            // wait would be theirs too.
+            gemm::wait_vmem<0>();
+            ahead = true;
             job.template finish<TL>(cc, acc, wm, wn, s_ring + 2 * TL::kStage + wave * TL::kOut);
         } else if (stages > 0) {
-            for (int64_t kt = 0; kt < stages; ++kt) {
+            for (int kt = 0; kt < stages; ++kt) {
                 read_barrier();
                 load_all();
                 stage_barrier<TL::kLoads>();
+                ahead = false;
                 advance();
-                cslot ^= 1;
+                ca = turn_a - ca;
+                cb = turn_b - cb;
             }
-            first_frags(s_ring + cslot * TL::kStage);  // the next tile's
         }
-        drain = true;
         cw += step;
         if (!job.next(cw, cc)) break;
     }
@@ -323,19 +354,26 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int64_t fir
 }
 
 // A wave's accumulators through its LDS buffer, 16 rows x 32 columns at a time: calls
-// put(row, col, v) with 8 neighbouring columns of a row of the tile.  The loop is rolled
-// (the block is picked by a switch), so that `put` stands in the code once.
-template <class TL, class Put>
-__device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int wm, int wn, uint8_t* out, Put put) {
+// put(row, col, v, x) with 8 neighbouring columns of a row of the tile and what
+// fetch(row, col, x) had asked for a block before.  The loop is rolled (the block is picked
+// by a chain of branches), so that `put` stands in the code once.
+template <class TL, class X, class Fetch, class Put>
+__device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int wm, int wn, uint8_t* out, Fetch fetch,
+                                           Put put) {
     constexpr int TM = TL::TM, TN = TL::TN;
     static_assert(TN % 2 == 0, "column blocks in pairs");
     const int lane = fresh_lane(), l16 = lane & 15, kg = lane >> 4;
     const int r = lane / 4, p = (lane & 3) * 2;
+    const int row0 = wm * TM * 16 + r, col0 = wn * TN * 16 + p * 4;
+    X x;
+    fetch(row0, col0, x);
 #pragma unroll 1
     for (int q = 0; q < TM * TN / 2; ++q) {
-        auto write = [&](const v4f& x, const v4f& y) {
-            *reinterpret_cast<v4f*>(out + l16 * 128 + (swz_chunk<128>(l16, kg) << 4)) = x;
-            *reinterpret_cast<v4f*>(out + l16 * 128 + (swz_chunk<128>(l16, kg + 4) << 4)) = y;
+        const X now = x;
+        if (q + 1 < TM * TN / 2) fetch(row0 + (q + 1) / (TN / 2) * 16, col0 + (q + 1) % (TN / 2) * 32, x);
+        auto write = [&](const v4f& a, const v4f& b) {
+            *reinterpret_cast<v4f*>(out + l16 * 128 + (swz_chunk<128>(l16, kg) << 4)) = a;
+            *reinterpret_cast<v4f*>(out + l16 * 128 + (swz_chunk<128>(l16, kg + 4) << 4)) = b;
         };
 #pragma unroll
         for (int j = 0; j < TM; ++j)
@@ -344,14 +382,130 @@ __device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int
                 if (q == j * (TN / 2) + i) {
                     // (the empty asm keeps the branches apart: merged, they would pick an address,
                     // and the accumulators would live in memory)
-                    v4f x = acc[2 * i][j], y = acc[2 * i + 1][j];
-                    __asm__ volatile("" : "+v"(x), "+v"(y));
-                    write(x, y);
+                    v4f a = acc[2 * i][j], b = acc[2 * i + 1][j];
+                    __asm__ volatile("" : "+v"(a), "+v"(b));
+                    write(a, b);
                 }
         const v4f lo = *reinterpret_cast<const v4f*>(out + r * 128 + (swz_chunk<128>(r, p) << 4));
         const v4f hi = *reinterpret_cast<const v4f*>(out + r * 128 + (swz_chunk<128>(r, p + 1) << 4));
         const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        put(wm * TM * 16 + q / (TN / 2) * 16 + r, wn * TN * 16 + q % (TN / 2) * 32 + p * 4, v);
+        put(row0 + q / (TN / 2) * 16, col0 + q % (TN / 2) * 32, v, now);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few tiles, or few rows: a small tile's depth is split over the waves of its workgroup.
+// Each wave takes every WAVES-th stage through two slots of its own, without a barrier,
+// and holds the whole tile; the waves' sums are joined in LDS in wave order.
+template <int BM_, int BN_, int WAVES_, bool AWIDE_, bool BWIDE_>
+struct SplitTile {
+    static constexpr int BM = BM_, BN = BN_, kWaves = WAVES_, kThreads = kWave * kWaves;
+    static constexpr int TM = BM / 16, TN = BN / 16;
+    using A = Operand<BM, AWIDE_, 1>;
+    using B = Operand<BN, BWIDE_, 1>;
+    static constexpr int kStage = A::kBytes + B::kBytes, kLoads = A::kLoads + B::kLoads;
+    static constexpr int kPitch = BN + 4;  // floats a row of a wave's sums
+    static constexpr int kRing = kWaves * 2 * kStage, kSums = kWaves * BM * kPitch * 4;
+    static constexpr int kLds = kRing > kSums ? kRing : kSums;
+};
+
+// One tile: put(row, col, v) is called with 8 neighbouring columns of its sums.
+template <class TL, class Job, class Put>
+__device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c, uint8_t* s_ring, Put put) {
+    constexpr int TM = TL::TM, TN = TL::TN;
+    using A = typename TL::A;
+    using B = typename TL::B;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t ring0 = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * 2 * TL::kStage);
+
+    // this wave's stages: `mine` of them; the producer is at depth `at` of segment c
+    const int mine = c.stages > wave ? (c.stages - wave + TL::kWaves - 1) / TL::kWaves : 0;
+    int at = wave * kStageDepth, issued = 0;
+    const int64_t sa = A::step(job.lda) / kStageDepth, sb = B::step(job.ldb) / kStageDepth;  // bytes a unit of depth
+    A fa;
+    B fb;
+    auto load = [&]() {  // the next of its stages into the slot of its turn; past the last one nothing, as zeros
+        bool more = issued < mine;
+        while (more && at >= c.depth) {  // groups of one expert follow each other, each in whole stages
+            at -= (c.depth + kStageDepth - 1) / kStageDepth * kStageDepth;
+            more = job.segment(c);
+        }
+        const int left = more ? c.depth - at : 0;
+        if (issued == 0 || left < kStageDepth || at < TL::kWaves * kStageDepth) {
+            fa.set(0, lane, c.rows_in, left, (uint32_t)job.lda);
+            fb.set(0, lane, c.cols_in, left, (uint32_t)job.ldb);
+        }
+        const uint64_t pa = (uint64_t)gemm::first_lane64((int64_t)c.a + at * sa);
+        const uint64_t pb = (uint64_t)gemm::first_lane64((int64_t)c.b + at * sb);
+        const v4i da = {(int)(uint32_t)pa, (int)(uint32_t)(pa >> 32), (int)kNowhere, 0x00020000};
+        const v4i db = {(int)(uint32_t)pb, (int)(uint32_t)(pb >> 32), (int)kNowhere, 0x00020000};
+        const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(ring0 + (issued & 1) * TL::kStage);
+        __asm__ volatile("s_nop 4");  // wait states of what the lane reads wrote
+#pragma unroll
+        for (int l = 0; l < A::kLoads; ++l) lds_load(da, fa.off[l], slot + l * 1024);
+#pragma unroll
+        for (int l = 0; l < B::kLoads; ++l) lds_load(db, fb.off[l], slot + A::kBytes + l * 1024);
+        ++issued;
+        at += TL::kWaves * kStageDepth;
+    };
+    const uint32_t abase = A::lane_base(lane, 0), bbase = B::lane_base(lane, 0);
+    v4f acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    load();
+    load();
+    for (int s = 0; s < mine; ++s) {
+        const uint32_t ca = ring0 + (s & 1) * TL::kStage + abase, cb = ca - abase + A::kBytes + bbase;
+        gemm::wait_vmem<TL::kLoads>();
+        __asm__ volatile("" ::: "memory");
+        v8b tf[2][TM], nf[2][TN];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i) nf[k][i] = B::frag(cb, i, k);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) tf[k][j] = A::frag(ca, j, k);
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the slot may be filled again
+        __asm__ volatile("" ::: "memory");
+        load();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[k][i], tf[k][j], acc[i][j], 0, 0, 0);
+    }
+    gemm::wait_vmem<0>();  // the last loads have landed: the sums may take their place
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(s_ring);
+    const int l16 = lane & 15, kg = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+            *reinterpret_cast<v4f*>(sums + (wave * TL::BM + j * 16 + l16) * TL::kPitch + i * 16 + kg * 4) = acc[i][j];
+    __syncthreads();
+    constexpr int kPieces = TL::BN / 8;
+    for (int q = threadIdx.x; q < TL::BM * kPieces; q += TL::kThreads) {
+        const int row = q / kPieces, col = q % kPieces * 8;
+        if (row >= c.rows_in || col >= c.cols_in) continue;
+        float v[8];
+#pragma unroll
+        for (int w = 0; w < TL::kWaves; ++w) {
+            const float* at8 = sums + (w * TL::BM + row) * TL::kPitch + col;
+            const v4f lo = *reinterpret_cast<const v4f*>(at8), hi = *reinterpret_cast<const v4f*>(at8 + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = w == 0 ? lo[i] : v[i] + lo[i];
+                v[4 + i] = w == 0 ? hi[i] : v[4 + i] + hi[i];
+            }
+        }
+        put(row, col, v);
     }
 }
 
