@@ -73,25 +73,27 @@ struct RowsJob {
     __device__ __forceinline__ void finish(const Coord& c, const v4f (&acc)[TL::TN][TL::TM], int wm, int wn,
                                            uint8_t* out) const {
         with_act(p.act, [&](auto act) {
-            if constexpr (BACK)
-                put_blocks<TL, Before>(
-                    acc, wm, wn, out,
-                    [&](int row, int col, Before& x) {
-                        if (row < c.rows_in && col < c.cols_in) fetch8_backward<act()>(p, c.m0 + row, c.n0 + col, x);
-                    },
-                    [&](int row, int col, const float* v, const Before& x) {
-                        if (row < c.rows_in && col < c.cols_in)
-                            finish8_backward<act()>(p, c.m0 + row, c.n0 + col, v, x);
+            if constexpr (BACK) {
+                put_rows<TL, Before<8>>(
+                    acc, wm, wn, c.rows_in, c.cols_in, out,
+                    [&](int row, int col, Before<8>& x) { fetch_backward<act(), 8>(p, c.m0 + row, c.n0 + col, x); },
+                    [&](int row, int col, const float* v, const Before<8>& x) {
+                        finish_backward<act(), 8>(p, c.m0 + row, c.n0 + col, v, x);
                     });
-            else
-                put_blocks<TL, Beside>(
-                    acc, wm, wn, out,
-                    [&](int row, int col, Beside& x) {
-                        if (row < c.rows_in && col < c.cols_in) fetch8<act()>(p, c.m0 + row, c.n0 + col, x);
-                    },
+            } else if ((p.N & 7) == 0) {
+                put_rows<TL, Beside>(
+                    acc, wm, wn, c.rows_in, c.cols_in, out,
+                    [&](int row, int col, Beside& x) { fetch8<act(), true>(p, c.e, c.m0 + row, c.n0 + col, x); },
                     [&](int row, int col, const float* v, const Beside& x) {
-                        if (row < c.rows_in && col < c.cols_in) finish8<act()>(p, c.e, c.m0 + row, c.n0 + col, v, x);
+                        finish8<act(), true>(p, c.m0 + row, c.n0 + col, v, x);
                     });
+            } else {
+                put_blocks<TL>(acc, wm, wn, c.rows_in, c.cols_in, out, [&](int row, int col, const float* v) {
+                    Beside x;
+                    fetch8<act(), false>(p, c.e, c.m0 + row, c.n0 + col, x);
+                    finish8<act(), false>(p, c.m0 + row, c.n0 + col, v, x);
+                });
+            }
         });
     }
 };

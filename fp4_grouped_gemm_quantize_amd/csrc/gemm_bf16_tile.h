@@ -135,7 +135,7 @@ struct Tile {
     static constexpr int kOut = 2048;  // bytes of LDS a wave's epilogue passes its results through
     static constexpr int kLds = 2 * kStage + kWaves * kOut;
     // column blocks of a stage's second step behind which the two barriers stand
-    static constexpr int kRead = TN >= 8 ? 1 : 0, kLanded = TN >= 4 ? TN - 3 : TN - 1;
+    static constexpr int kRead = TN >= 8 ? 1 : 0, kLanded = TN >= 8 ? 3 : TN >= 4 ? 1 : TN - 1;
     // A stage's loads are spread over the column blocks from kRead on, about one a block: the loads'
     // path moves 64 bytes a cycle, and waves that issue faster wait.  How many stand before block i:
     static constexpr int loads_before(int i) { return kLoads * (i - kRead) / (TN - kRead); }
@@ -265,11 +265,21 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     // fragments' own addresses are made where they are read and hold no registers)
     uint32_t ca = gemm::lds_addr(s_ring) + abase, cb = gemm::lds_addr(s_ring) + A::kBytes + bbase;
     const uint32_t turn_a = 2 * ca + TL::kStage, turn_b = 2 * cb + TL::kStage;
+    // a stage begins with these fragments in registers, read in this order; the rest follow in it
+    constexpr int kPre = TN < 3 ? TN : 3;
     auto first_frags = [&]() {
+        nf[0] = B::frag(cb, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < TN; ++i) nf[i] = B::frag(cb, i, 0);
+        for (int j = 0; j < TM; ++j) {
+            tf[0][j] = A::frag(ca, j, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-        for (int j = 0; j < TM; ++j) tf[0][j] = A::frag(ca, j, 0);
+        for (int i = 1; i < kPre; ++i) {
+            nf[i] = B::frag(cb, i, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     bool ahead = false;  // the next stage has landed already
     for (;;) {
@@ -299,6 +309,7 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
                     for (int j = 0; j < TM; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[i], tf[0][j], acc[i][j], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
+                    if (i + kPre < TN) nf[i + kPre] = B::frag(cb, i + kPre, 0);
                     nf[i] = B::frag(cb, i, 1);
 #pragma unroll
                     for (int j = i * TM / TN; j < (i + 1) * TM / TN; ++j) tf[1][j] = A::frag(ca, j, 1);
@@ -318,13 +329,18 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
                         if (!ahead) gemm::wait_vmem<TL::loads_before(TL::kLanded + 1)>();
                         ahead = false;
                         read_barrier();
-                        nf[0] = B::frag(nb, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < TM; ++j) tf[0][j] = A::frag(na, j, 0);
-#pragma unroll
-                        for (int f = 1; f <= i; ++f) nf[f] = B::frag(nb, f, 0);
                     }
-                    if (i > TL::kLanded) nf[i] = B::frag(nb, i, 0);
+                    if (i >= TL::kLanded) {
+                        // the next stage's first fragments (nf[0], tf, nf[1] ...), over the blocks left
+                        constexpr int kAll = TM + kPre, kLeft = TN - TL::kLanded;
+#pragma unroll
+                        for (int q = (i - TL::kLanded) * kAll / kLeft; q < (i - TL::kLanded + 1) * kAll / kLeft; ++q) {
+                            if (q == 0) nf[0] = B::frag(nb, 0, 0);
+                            else if (q <= TM) tf[0][q > 0 && q <= TM ? q - 1 : 0] = A::frag(na, q - 1, 0);
+                            else nf[q > TM ? q - TM : 0] = B::frag(nb, q - TM, 0);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 advance();
@@ -353,24 +369,65 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     gemm::wait_vmem<0>();  // no load may land once the workgroup's LDS belongs to another
 }
 
-// A wave's accumulators through its LDS buffer, 16 rows x 32 columns at a time: calls
-// put(row, col, v, x) with 8 neighbouring columns of a row of the tile and what
-// fetch(row, col, x) had asked for a block before.  The loop is rolled (the block is picked
-// by a chain of branches), so that `put` stands in the code once.
+// A wave's accumulators through its LDS buffer, 8 rows x 64 columns at a time (16 x 32 where the
+// wave has fewer columns): put(row, col, v, x) gets 8 neighbouring columns of a row of the tile
+// and what fetch(row, col, x) asked for a block before, so that a row of bf16 goes out in whole
+// lines of 128 bytes.  LDS serves a wave in order: a block's writes need not wait for the reads
+// of the one before.
 template <class TL, class X, class Fetch, class Put>
-__device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int wm, int wn, uint8_t* out, Fetch fetch,
-                                           Put put) {
+__device__ __forceinline__ void put_rows(const v4f (&acc)[TL::TN][TL::TM], int wm, int wn, int rows, int cols,
+                                         uint8_t* out, Fetch fetch, Put put) {
+    constexpr int TM = TL::TM, TN = TL::TN;
+    constexpr int kFrags = TN % 4 == 0 ? 4 : 2, kRows = 32 / kFrags, kLanes = kFrags * 2;  // lanes a row
+    constexpr int kHalves = 16 / kRows, kAcross = TN / kFrags, kBlocks = TM * kHalves * kAcross;
+    static_assert(TN % 2 == 0, "column blocks in pairs");
+    const int lane = fresh_lane(), l16 = lane & 15, kg = lane >> 4;
+    const int r = lane / kLanes, c = lane % kLanes;
+    const int row0 = wm * TM * 16 + r, col0 = wn * TN * 16 + c * 8;
+    // 16-byte pieces of a row: XORed so that a 16-lane slice of a write (four rows, or more, by four
+    // pieces) and of a read (every other piece of two rows or more) lies in distinct banks
+    auto at = [&](int row, int piece) -> uint8_t* {
+        const int turn = kFrags == 4 ? (row & 3) << 2 | (row & 1) : (row >> 1) & 7;
+        return out + row * (kFrags * 64) + ((piece ^ turn) << 4);
+    };
+    X x[2];
+    auto place = [&](int q, int& row, int& col) {  // halves of 16 rows innermost, then across
+        row = row0 + q / (kHalves * kAcross) * 16 + q % kHalves * kRows;
+        col = col0 + q / kHalves % kAcross * (kFrags * 16);
+    };
+    auto ask = [&](int q) {
+        int row, col;
+        place(q, row, col);
+        if (row < rows && col < cols) fetch(row, col, x[q & 1]);
+    };
+    ask(0);
+#pragma unroll
+    for (int q = 0; q < kBlocks; ++q) {
+        const int j = q / (kHalves * kAcross), i = q / kHalves % kAcross * kFrags;
+        if (q + 1 < kBlocks) ask(q + 1);
+        if (kHalves == 1 || l16 / kRows == q % kHalves)
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f)
+                *reinterpret_cast<v4f*>(at(l16 % kRows, f * 4 + kg)) = acc[i + f][j];
+        const v4f lo = *reinterpret_cast<const v4f*>(at(r, 2 * c)), hi = *reinterpret_cast<const v4f*>(at(r, 2 * c + 1));
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        int row, col;
+        place(q, row, col);
+        if (row < rows && col < cols) put(row, col, v, x[q & 1]);
+    }
+}
+
+// The same for rows that are no whole vectors.  The loop is rolled (the block is
+// picked by a chain of branches), so that `put` stands in the code once.
+template <class TL, class Put>
+__device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int wm, int wn, int rows, int cols,
+                                           uint8_t* out, Put put) {
     constexpr int TM = TL::TM, TN = TL::TN;
     static_assert(TN % 2 == 0, "column blocks in pairs");
     const int lane = fresh_lane(), l16 = lane & 15, kg = lane >> 4;
     const int r = lane / 4, p = (lane & 3) * 2;
-    const int row0 = wm * TM * 16 + r, col0 = wn * TN * 16 + p * 4;
-    X x;
-    fetch(row0, col0, x);
 #pragma unroll 1
     for (int q = 0; q < TM * TN / 2; ++q) {
-        const X now = x;
-        if (q + 1 < TM * TN / 2) fetch(row0 + (q + 1) / (TN / 2) * 16, col0 + (q + 1) % (TN / 2) * 32, x);
         auto write = [&](const v4f& a, const v4f& b) {
             *reinterpret_cast<v4f*>(out + l16 * 128 + (swz_chunk<128>(l16, kg) << 4)) = a;
             *reinterpret_cast<v4f*>(out + l16 * 128 + (swz_chunk<128>(l16, kg + 4) << 4)) = b;
@@ -389,7 +446,8 @@ __device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int
         const v4f lo = *reinterpret_cast<const v4f*>(out + r * 128 + (swz_chunk<128>(r, p) << 4));
         const v4f hi = *reinterpret_cast<const v4f*>(out + r * 128 + (swz_chunk<128>(r, p + 1) << 4));
         const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        put(row0 + q / (TN / 2) * 16, col0 + q % (TN / 2) * 32, v, now);
+        const int row = wm * TM * 16 + q / (TN / 2) * 16 + r, col = wn * TN * 16 + q % (TN / 2) * 32 + p * 4;
+        if (row < rows && col < cols) put(row, col, v);
     }
 }
 

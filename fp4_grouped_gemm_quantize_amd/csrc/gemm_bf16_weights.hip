@@ -28,22 +28,25 @@ struct WeightsArgs {
     int ntn, ntk;  // tiles along N and K
 };
 
-// 8 neighbouring columns of dw out; old: what they held, asked for ahead.
-__device__ __forceinline__ uint8_t* at8(const WeightsArgs& p, int e, int64_t n, int64_t k) {
+// W neighbouring columns of dw out; old: what they held, asked for ahead.
+template <int W>
+struct Old {
+    float v[W];
+};
+__device__ __forceinline__ uint8_t* dw_at(const WeightsArgs& p, int e, int64_t n, int64_t k) {
     return static_cast<uint8_t*>(p.dw) + (((int64_t)e * p.N + n) * p.K + k) * (p.dw32 ? 4 : 2);
 }
-struct Old {
-    float v[8];
-};
-__device__ __forceinline__ void fetch8(const WeightsArgs& p, int e, int64_t n, int64_t k, Old& old) {
-    if (p.accumulate) load_n<8>(at8(p, e, n, k), p.dw32, true, 8, old.v);
+template <int W>
+__device__ __forceinline__ void fetch(const WeightsArgs& p, int e, int64_t n, int64_t k, Old<W>& old) {
+    if (p.accumulate) load_n<W>(dw_at(p, e, n, k), p.dw32, true, W, old.v);
 }
-__device__ __forceinline__ void put8(const WeightsArgs& p, int e, int64_t n, int64_t k, const float* sums,
-                                     const Old& old) {
-    float v[8];
+template <int W>
+__device__ __forceinline__ void write(const WeightsArgs& p, int e, int64_t n, int64_t k, const float* sums,
+                                       const Old<W>& old) {
+    float v[W];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p.accumulate ? sums[i] + old.v[i] : sums[i];
-    store_n<8>(at8(p, e, n, k), p.dw32, true, 8, v);
+    for (int i = 0; i < W; ++i) v[i] = p.accumulate ? sums[i] + old.v[i] : sums[i];
+    store_n<W>(dw_at(p, e, n, k), p.dw32, true, W, v);
 }
 
 template <class TL>
@@ -116,13 +119,11 @@ struct WeightsJob {
     __device__ __forceinline__ void finish(const Coord& c, const v4f (&acc)[TL::TN][TL::TM], int wm, int wn,
                                            uint8_t* out) const {
         if (p.accumulate && c.stages == 0) return;
-        put_blocks<TL, Old>(
-            acc, wm, wn, out,
-            [&](int row, int col, Old& old) {
-                if (row < c.rows_in && col < c.cols_in) fetch8(p, c.e, c.n0 + row, c.k0 + col, old);
-            },
-            [&](int row, int col, const float* v, const Old& old) {
-                if (row < c.rows_in && col < c.cols_in) put8(p, c.e, c.n0 + row, c.k0 + col, v, old);
+        put_rows<TL, Old<8>>(
+            acc, wm, wn, c.rows_in, c.cols_in, out,
+            [&](int row, int col, Old<8>& old) { fetch(p, c.e, c.n0 + row, c.k0 + col, old); },
+            [&](int row, int col, const float* v, const Old<8>& old) {
+                write(p, c.e, c.n0 + row, c.k0 + col, v, old);
             });
     }
 };
@@ -160,9 +161,9 @@ __global__ __launch_bounds__(TL::kThreads, 1) void weights_split_kernel(const We
     job.locate(gemm::xcd_remap((int)blockIdx.x, (int)gridDim.x), c);
     if (p.accumulate && c.stages == 0) return;
     run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
-        Old old;
-        fetch8(p, c.e, c.n0 + row, c.k0 + col, old);
-        put8(p, c.e, c.n0 + row, c.k0 + col, v, old);
+        Old<8> old;
+        fetch(p, c.e, c.n0 + row, c.k0 + col, old);
+        write(p, c.e, c.n0 + row, c.k0 + col, v, old);
     });
 }
 
