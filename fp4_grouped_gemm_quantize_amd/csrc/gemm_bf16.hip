@@ -19,6 +19,7 @@ struct RowsJob {
         int e, rows_in, cols_in, m0, n0, stages, depth;
         const uint8_t *a, *b;
     };
+    static constexpr bool kSums = false;
     const Bf16Problem& p;
     const uint32_t* s_pre;  // M tiles before each group, then of all
     const uint32_t* s_off;
@@ -98,18 +99,27 @@ struct RowsJob {
     }
 };
 
-template <class TL, bool BACK>
-__global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16Problem p, int ntn, int mband) {
-    __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
-    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
-    __shared__ int32_t s_ids[kMaxGroups];
+// The routing and the M tiles before each group into LDS; returns how many tiles there are.
+template <class TL>
+__device__ __forceinline__ int load_groups(const Bf16Problem& p, uint32_t* s_pre, uint32_t* s_off, int32_t* s_ids,
+                                           uint32_t* s_wave) {
     const int tid = threadIdx.x, G = p.G;
+    if (p.off == nullptr) {  // one group
+        const int total = (int)((p.T + TL::BM - 1) / TL::BM);
+        if (tid == 0) {
+            s_off[0] = s_pre[0] = 0;
+            s_off[1] = (uint32_t)p.T;
+            s_pre[1] = (uint32_t)total;
+            s_ids[0] = 0;
+        }
+        __syncthreads();
+        return total;
+    }
     for (int i = tid; i <= G; i += TL::kThreads) {
-        s_off[i] = p.off ? p.off[i] : i ? (uint32_t)p.T : 0;
-        if (i < G) s_ids[i] = p.ids ? p.ids[i] : 0;
+        s_off[i] = p.off[i];
+        if (i < G) s_ids[i] = p.ids[i];
     }
     __syncthreads();
-    // M tiles before each group
     constexpr int kPer = (kMaxGroups + TL::kThreads - 1) / TL::kThreads;
     uint32_t cnt[kPer], local = 0, total;
 #pragma unroll
@@ -131,10 +141,53 @@ __global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16
     }
     if (tid == 0) s_pre[G] = total;
     __syncthreads();
+    return (int)total;
+}
+
+template <class TL, bool BACK>
+__global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16Problem p, int ntn, int mband) {
+    __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
+    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
+    __shared__ int32_t s_ids[kMaxGroups];
+    const int total = load_groups<TL>(p, s_pre, s_off, s_ids, s_wave);
     const int cols = (int)(BACK ? p.K : p.N), deep = (int)(BACK ? p.N : p.K), grid = (int)gridDim.x;
-    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, items_of((int)total * ntn, grid),
+    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, items_of(total * ntn, grid),
                           (int64_t)deep * 2, (int64_t)(BACK ? cols : deep) * 2, cols, deep, grid};
     run_tiles<TL>(job, s_ring, gemm::xcd_remap((int)blockIdx.x, grid), grid);
+}
+
+// Small tiles, one a workgroup, their depth split over its waves.
+template <class TL, bool BACK>
+__global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_split_kernel(const Bf16Problem p, int ntn) {
+    __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
+    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
+    __shared__ int32_t s_ids[kMaxGroups];
+    const int total = load_groups<TL>(p, s_pre, s_off, s_ids, s_wave) * ntn;
+    const int W = gemm::xcd_remap((int)blockIdx.x, (int)gridDim.x);
+    if (W >= total) return;  // workgroup-uniform
+    const int cols = (int)(BACK ? p.K : p.N), deep = (int)(BACK ? p.N : p.K);
+    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, 1 << 20, {total, total},
+                          (int64_t)deep * 2, (int64_t)(BACK ? cols : deep) * 2, cols, deep, total};
+    typename RowsJob<TL, BACK>::Coord c;
+    job.locate(W, c);
+    with_act(p.act, [&](auto act) {
+        run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
+            if constexpr (BACK) {
+                Before<8> x;
+                fetch_backward<act(), 8>(p, c.m0 + row, c.n0 + col, x);
+                finish_backward<act(), 8>(p, c.m0 + row, c.n0 + col, v, x);
+            } else {
+                Beside x;
+                if ((p.N & 7) == 0) {
+                    fetch8<act(), true>(p, c.e, c.m0 + row, c.n0 + col, x);
+                    finish8<act(), true>(p, c.m0 + row, c.n0 + col, v, x);
+                } else {
+                    fetch8<act(), false>(p, c.e, c.m0 + row, c.n0 + col, x);
+                    finish8<act(), false>(p, c.m0 + row, c.n0 + col, v, x);
+                }
+            }
+        });
+    });
 }
 
 int64_t compute_units() {
@@ -153,6 +206,16 @@ hipError_t launch_tile(const Bf16Problem& p, int per_cu, int mband, hipStream_t 
     return hipGetLastError();
 }
 
+template <class TL, bool BACK>
+hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
+    const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
+    const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
+    if (most > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
+    hipLaunchKernelGGL((matmul_bf16_split_kernel<TL, BACK>), dim3((unsigned)most), dim3(TL::kThreads), 0, stream, p,
+                       (int)ntn);
+    return hipGetLastError();
+}
+
 template <bool BACK>
 hipError_t launch(const Bf16Problem& p, hipStream_t stream) {
     using Large = Tile<256, 256, 4, 2, false, BACK>;
@@ -162,6 +225,11 @@ hipError_t launch(const Bf16Problem& p, hipStream_t stream) {
     const int t = f ? atoi(f) : 256;
     if (t == 128) return launch_tile<Mid, BACK>(p, 2, 4, stream);
     if (t == 32) return launch_tile<Small, BACK>(p, 3, 1 << 30, stream);
+    if (t == 6464) return launch_split<SplitTile<64, 64, 4, false, BACK>, BACK>(p, stream);
+    if (t == 6432) return launch_split<SplitTile<64, 32, 5, false, BACK>, BACK>(p, stream);
+    if (t == 3232) return launch_split<SplitTile<32, 32, 8, false, BACK>, BACK>(p, stream);
+    if (t == 1632) return launch_split<SplitTile<16, 32, 8, false, BACK>, BACK>(p, stream);
+    if (t == 1664) return launch_split<SplitTile<16, 64, 6, false, BACK>, BACK>(p, stream);
     return launch_tile<Large, BACK>(p, 1, 4, stream);
 }
 

@@ -9,10 +9,11 @@
 //    16-byte pieces XOR-swizzled, read 16 bytes a lane) or wide (the depth is its row
 //    index: stage rows of R elements, 32-byte pieces XOR-swizzled, read through the
 //    transposing LDS load, which gives a lane four depths of its column).
-//  * Loads go through buffer descriptors: a lane whose row, column or depth lies past
-//    the operand asks for an offset past the descriptor's range, which reads nothing and
-//    leaves zeros in LDS.  So rows and tails of any size need no second path, and what
-//    lies behind them (another expert's rows, whatever they hold) takes no part.
+//  * Loads go through buffer descriptors whose range ends behind the tile's rows (or its
+//    depth); a lane whose piece lies past the columns (or the depth) asks for an offset
+//    past every range.  What is past the range reads nothing and leaves zeros in LDS, so
+//    rows and tails of any size need no second path, and what lies behind them (another
+//    expert's rows, whatever they hold) takes no part.
 //  * A stage is two steps of 32 in depth.  While a step is multiplied, the next step's
 //    fragments replace its own, one by one.  Two barriers a stage: behind the first
 //    (all waves have read the slot) its slot is filled with the stage after the next;
@@ -36,14 +37,14 @@ constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every descriptor's
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
-// A direct-to-LDS load of 16 bytes a lane (lane l to lds + 16 l) through a buffer descriptor;
-// both in scalar registers that no vector instruction has just written.
-__device__ __forceinline__ void lds_load(const v4i& desc, uint32_t off, uint32_t lds) {
+// A direct-to-LDS load of 16 bytes a lane (lane l to lds + 16 l) at off + soff from a buffer
+// descriptor's base; all but off in scalar registers that no vector instruction has just written.
+__device__ __forceinline__ void lds_load(const v4i& desc, uint32_t off, uint32_t soff, uint32_t lds) {
     __asm__ volatile(
-        "s_mov_b32 m0, %2\n\ts_nop 0\n\t"
-        "buffer_load_dwordx4 %0, %1, 0 offen lds"
+        "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %0, %1, %2 offen lds"
         :
-        : "v"(off), "s"(desc), "s"(lds)
+        : "v"(off), "s"(desc), "s"(soff), "s"(lds)
         : "memory", "m0");
 }
 
@@ -56,7 +57,7 @@ struct Operand {
     static constexpr int kLanes = kRowBytes / 16;                // lanes a stage row
     static constexpr int kRows = 64 / kLanes;                    // stage rows a load
     static_assert(kLoads * NW * 1024 == kBytes, "whole loads");
-    static_assert(R >= 32, "a wide stage row holds two pieces of 32 bytes at least");
+    static_assert(!WIDE || R >= 32, "a wide stage row holds two pieces of 32 bytes at least");
 
     // Wide rows: the 32-byte pieces of a row are XORed with this, so that the eight rows
     // that half a wave reads at one column ({0..3} and {8..11} beside a multiple of 4)
@@ -69,7 +70,11 @@ struct Operand {
     }
 
     static constexpr bool kWide = WIDE;
-    uint32_t off[kLoads];
+    static constexpr int kStep = NW * kRows;                     // stage rows from a load to a wave's next
+    // the swizzles repeat every 16 rows: so many of a wave's loads differ by more than their row
+    static constexpr int kOffs = kStep % 16 == 0 ? 1 : kStep % 8 == 0 ? 2 : 4;
+    static_assert(kStep % 4 == 0 && (kLoads % kOffs == 0 || kLoads < kOffs), "whole turns of the swizzle");
+    uint32_t off[kOffs];
 
     static __device__ __forceinline__ int stage_row(int wave, int lane, int j) {
         return (wave + NW * j) * kRows + lane / kLanes;
@@ -79,14 +84,23 @@ struct Operand {
         if constexpr (WIDE) return (lane % kLanes) ^ (turn(row) << 1);
         else return swz_chunk<128>(row, lane % 8);
     }
-    // Offsets of a stage at whose base `real` rows (columns) and `depth` deep are left; ld: bytes a source row.
-    __device__ __forceinline__ void set(int wave, int lane, int real, int depth, uint32_t ld) {
+    // This lane's offsets in a tile of `real` columns (wide), in a stage with `left` of the depth before it
+    // (deep: its pieces past the end ask for what lies past the range).
+    __device__ __forceinline__ void set(int wave, int lane, int real, int left, uint32_t ld) {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < kOffs; ++j) {
             const int row = stage_row(wave, lane, j), p = piece(row, lane);
-            const int across = WIDE ? p * 8 : row, deep = WIDE ? row : p * 8;
-            off[j] = across < real && deep < depth ? (uint32_t)row * ld + p * 16 : kNowhere;
+            off[j] = p * 8 < (WIDE ? real : left) ? (uint32_t)row * ld + p * 16 : kNowhere;
         }
+    }
+    // The descriptor's range, from the stage's base: it ends behind the tile's last row (deep: behind the
+    // end of that row, `left` of whose depth lies before it), or behind the depth's last row (wide).
+    static __device__ __forceinline__ int range(int real, int left, int depth, uint32_t ld) {
+        if constexpr (WIDE) return (left < kStageDepth ? left : kStageDepth) * (int)ld;
+        else return (int)((uint32_t)real * ld - (uint32_t)(depth - left) * 2);
+    }
+    __device__ __forceinline__ void load(const v4i& desc, int j, uint32_t ld, uint32_t lds) const {
+        lds_load(desc, off[j % kOffs], (uint32_t)(j / kOffs * kOffs * kStep) * ld, lds + j * (NW * 1024));
     }
     // bytes the base moves a stage
     static __device__ __forceinline__ int64_t step(int64_t ld) { return WIDE ? kStageDepth * ld : 128; }
@@ -151,6 +165,19 @@ __device__ __forceinline__ Items items_of(int tiles, int grid) {
     return rest > 0 && 2 * rest <= grid ? Items{tiles - rest, tiles + rest} : Items{tiles, tiles};
 }
 
+// The sum of a fragment's 8 values in this lane's row.
+__device__ __forceinline__ float frag_sum(const v8b& f) {
+    union {
+        v8b b;
+        uint32_t w[4];
+    } u;
+    u.b = f;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += __uint_as_float(u.w[i] << 16) + __uint_as_float(u.w[i] & 0xffff0000u);
+    return s;
+}
+
 // The lane number, made anew where it is needed: what derives from it holds no register
 // between stages.
 __device__ __forceinline__ int fresh_lane() {
@@ -166,6 +193,8 @@ __device__ __forceinline__ int fresh_lane() {
 //   bool segment(Coord&)            the tile's next stretch of depth, or false
 //   lda, ldb                        bytes a row of the operands
 //   void finish(c, acc, wm, wn, out)   epilogue of a wave's accumulators
+//   kSums, bool sums(c), void put_sum(c, row, v)   whether A's rows are added up over the depth
+//                beside the product, in which tiles, and where a sum goes
 template <class TL, class Job>
 __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, int step) {
     constexpr int TM = TL::TM, TN = TL::TN;
@@ -178,21 +207,24 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     int cw = first;
     if (!job.next(cw, cc)) return;  // workgroup-uniform
 
-    // ---- the producer: two stages ahead.  Pointers, offsets and `left` (depth from its stage to
-    // the segment's end) are those of its next stage; past the last tile every lane asks for
-    // nothing, so that its loads need no branch.
+    // ---- the producer: two stages ahead.  Pointers, ranges, offsets and `left` (depth from its stage to
+    // the segment's end) are those of its next stage; past the last tile `left` is 0 and its loads
+    // have an empty range, so that they need no branch.
     typename Job::Coord pc = cc;
-    int pw = cw, left = 0;
+    int pw = cw, left = 0, ra = 0, rb = 0;  // ra, rb: the ranges
     uint64_t pa = 0, pb = 0;
     uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * 1024);
     const uint32_t slots = 2 * slot + TL::kStage;  // slot + the other slot
     const int64_t sa = gemm::first_lane64(A::step(job.lda)), sb = gemm::first_lane64(B::step(job.ldb));
     A fa;
     B fb;
+    const uint32_t lda = (uint32_t)job.lda, ldb = (uint32_t)job.ldb;
     auto offsets = [&]() {
         const int lane = fresh_lane();
-        fa.set(wave, lane, pc.rows_in, left, (uint32_t)job.lda);
-        fb.set(wave, lane, pc.cols_in, left, (uint32_t)job.ldb);
+        fa.set(wave, lane, pc.rows_in, left, lda);
+        fb.set(wave, lane, pc.cols_in, left, ldb);
+        ra = __builtin_amdgcn_readfirstlane(A::range(pc.rows_in, left, pc.depth, lda));
+        rb = __builtin_amdgcn_readfirstlane(B::range(pc.cols_in, left, pc.depth, ldb));
     };
     auto begin = [&]() {  // the first stage of pc's segment
         pa = (uint64_t)gemm::first_lane64((int64_t)pc.a);
@@ -205,10 +237,8 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
             pw += step;
             more = job.next(pw, pc);
         }
-        if (more) return begin();
-        pc.rows_in = pc.cols_in = 0;
-        left = 1 << 30;
-        offsets();
+        if (more) begin();
+        else left = ra = rb = 0;
     };
     struct Where {
         v4i da, db;
@@ -217,15 +247,16 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     auto where = [&]() {
         // (scalar already; the lane reads say so where the compiler cannot tell)
         const uint64_t ua = (uint64_t)gemm::first_lane64((int64_t)pa), ub = (uint64_t)gemm::first_lane64((int64_t)pb);
-        const Where w = {{(int)(uint32_t)ua, (int)(uint32_t)(ua >> 32), (int)kNowhere, 0x00020000},
-                         {(int)(uint32_t)ub, (int)(uint32_t)(ub >> 32), (int)kNowhere, 0x00020000},
-                         (uint32_t)__builtin_amdgcn_readfirstlane(slot)};
+        const Where w = {
+            {(int)(uint32_t)ua, (int)(uint32_t)(ua >> 32), __builtin_amdgcn_readfirstlane(ra), 0x00020000},
+            {(int)(uint32_t)ub, (int)(uint32_t)(ub >> 32), __builtin_amdgcn_readfirstlane(rb), 0x00020000},
+            (uint32_t)__builtin_amdgcn_readfirstlane(slot)};
         __asm__ volatile("s_nop 4");  // wait states of what a lane read wrote
         return w;
     };
     auto load = [&](const Where& w, int l) {
-        if (l < A::kLoads) lds_load(w.da, fa.off[l < A::kLoads ? l : 0], w.slot + l * (TL::kWaves * 1024));
-        else lds_load(w.db, fb.off[l < A::kLoads ? 0 : l - A::kLoads], w.slot + l * (TL::kWaves * 1024));
+        if (l < A::kLoads) fa.load(w.da, l, lda, w.slot);
+        else fb.load(w.db, l - A::kLoads, ldb, w.slot + A::kBytes);
     };
     auto load_all = [&]() {
         const Where w = where();
@@ -236,7 +267,10 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
         slot = slots - slot;
         pa += sa;
         pb += sb;
+        if (left == 0) return;  // past the last tile
         left -= kStageDepth;
+        if (!A::kWide) ra -= kStageDepth * 2;
+        if (!B::kWide) rb -= kStageDepth * 2;
         if (left < kStageDepth) {
             if (left > 0) offsets();  // a last stage that is not whole
             else if (job.segment(pc)) begin();
@@ -290,6 +324,9 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
 #pragma unroll
             for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
         const int stages = __builtin_amdgcn_readfirstlane(cc.stages);
+        float sum[Job::kSums ? TM : 1] = {};
+        bool add_up = false;
+        if constexpr (Job::kSums) add_up = wn == 0 && job.sums(cc);
         auto read_barrier = [&]() {
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's fragments are in registers
             __asm__ volatile("" ::: "memory");
@@ -315,6 +352,10 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
                     for (int j = i * TM / TN; j < (i + 1) * TM / TN; ++j) tf[1][j] = A::frag(ca, j, 1);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                if constexpr (Job::kSums)
+                    if (add_up)
+#pragma unroll
+                        for (int j = 0; j < TM; ++j) sum[j] += frag_sum(tf[0][j]) + frag_sum(tf[1][j]);
 #pragma unroll
                 for (int i = 0; i < TN; ++i) {
 #pragma unroll
@@ -352,6 +393,16 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
             gemm::wait_vmem<0>();
             ahead = true;
             job.template finish<TL>(cc, acc, wm, wn, s_ring + 2 * TL::kStage + wave * TL::kOut);
+            if constexpr (Job::kSums)
+                if (add_up)
+#pragma unroll
+                    for (int j = 0; j < TM; ++j) {
+                        float v = sum[j];  // four lanes a row
+                        v += __shfl_xor(v, 16, kWave);
+                        v += __shfl_xor(v, 32, kWave);
+                        const int lane = fresh_lane(), row = (wm * TM + j) * 16 + (lane & 15);
+                        if (lane < 16 && row < cc.rows_in) job.put_sum(cc, row, v);
+                    }
         } else if (stages > 0) {
             for (int kt = 0; kt < stages; ++kt) {
                 read_barrier();
@@ -481,6 +532,7 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
     const int mine = c.stages > wave ? (c.stages - wave + TL::kWaves - 1) / TL::kWaves : 0;
     int at = wave * kStageDepth, issued = 0;
     const int64_t sa = A::step(job.lda) / kStageDepth, sb = B::step(job.ldb) / kStageDepth;  // bytes a unit of depth
+    const uint32_t lda = (uint32_t)job.lda, ldb = (uint32_t)job.ldb;
     A fa;
     B fb;
     auto load = [&]() {  // the next of its stages into the slot of its turn; past the last one nothing, as zeros
@@ -491,19 +543,21 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
         }
         const int left = more ? c.depth - at : 0;
         if (issued == 0 || left < kStageDepth || at < TL::kWaves * kStageDepth) {
-            fa.set(0, lane, c.rows_in, left, (uint32_t)job.lda);
-            fb.set(0, lane, c.cols_in, left, (uint32_t)job.ldb);
+            fa.set(0, lane, c.rows_in, left, lda);
+            fb.set(0, lane, c.cols_in, left, ldb);
         }
         const uint64_t pa = (uint64_t)gemm::first_lane64((int64_t)c.a + at * sa);
         const uint64_t pb = (uint64_t)gemm::first_lane64((int64_t)c.b + at * sb);
-        const v4i da = {(int)(uint32_t)pa, (int)(uint32_t)(pa >> 32), (int)kNowhere, 0x00020000};
-        const v4i db = {(int)(uint32_t)pb, (int)(uint32_t)(pb >> 32), (int)kNowhere, 0x00020000};
+        const int ra = __builtin_amdgcn_readfirstlane(more ? A::range(c.rows_in, left, c.depth, lda) : 0);
+        const int rb = __builtin_amdgcn_readfirstlane(more ? B::range(c.cols_in, left, c.depth, ldb) : 0);
+        const v4i da = {(int)(uint32_t)pa, (int)(uint32_t)(pa >> 32), ra, 0x00020000};
+        const v4i db = {(int)(uint32_t)pb, (int)(uint32_t)(pb >> 32), rb, 0x00020000};
         const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(ring0 + (issued & 1) * TL::kStage);
         __asm__ volatile("s_nop 4");  // wait states of what the lane reads wrote
 #pragma unroll
-        for (int l = 0; l < A::kLoads; ++l) lds_load(da, fa.off[l], slot + l * 1024);
+        for (int l = 0; l < A::kLoads; ++l) fa.load(da, l, lda, slot);
 #pragma unroll
-        for (int l = 0; l < B::kLoads; ++l) lds_load(db, fb.off[l], slot + A::kBytes + l * 1024);
+        for (int l = 0; l < B::kLoads; ++l) fb.load(db, l, ldb, slot + A::kBytes);
         ++issued;
         at += TL::kWaves * kStageDepth;
     };
@@ -513,6 +567,9 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    float sum[Job::kSums ? TM : 1] = {};
+    bool add_up = false;
+    if constexpr (Job::kSums) add_up = job.sums(c);
     load();
     load();
     for (int s = 0; s < mine; ++s) {
@@ -537,6 +594,10 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
 #pragma unroll
                 for (int j = 0; j < TM; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[k][i], tf[k][j], acc[i][j], 0, 0, 0);
+        if constexpr (Job::kSums)
+            if (add_up)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) sum[j] += frag_sum(tf[0][j]) + frag_sum(tf[1][j]);
     }
     gemm::wait_vmem<0>();  // the last loads have landed: the sums may take their place
     __syncthreads();
@@ -547,7 +608,20 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
 #pragma unroll
         for (int j = 0; j < TM; ++j)
             *reinterpret_cast<v4f*>(sums + (wave * TL::BM + j * 16 + l16) * TL::kPitch + i * 16 + kg * 4) = acc[i][j];
+    if constexpr (Job::kSums)  // a row's partial sums: beside its columns, by lane group
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+            sums[(wave * TL::BM + j * 16 + l16) * TL::kPitch + TL::BN + kg] = sum[j];
     __syncthreads();
+    if constexpr (Job::kSums)
+        if (add_up && (int)threadIdx.x < c.rows_in && threadIdx.x < TL::BM) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < TL::kWaves; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v += sums[(w * TL::BM + (int)threadIdx.x) * TL::kPitch + TL::BN + i];
+            job.put_sum(c, (int)threadIdx.x, v);
+        }
     constexpr int kPieces = TL::BN / 8;
     for (int q = threadIdx.x; q < TL::BM * kPieces; q += TL::kThreads) {
         const int row = q / kPieces, col = q % kPieces * 8;

@@ -49,15 +49,17 @@ __device__ __forceinline__ void write(const WeightsArgs& p, int e, int64_t n, in
     store_n<W>(dw_at(p, e, n, k), p.dw32, true, W, v);
 }
 
-template <class TL>
+template <class TL, bool BIAS>
 struct WeightsJob {
+    static constexpr bool kSums = BIAS;
     struct Coord {
         int e, g, rows_in, cols_in, n0, k0, stages, depth;  // g: the group of the present segment
         const uint8_t *a, *b;
     };
     const WeightsArgs& p;
-    const uint32_t* s_off;  // clamped to T
+    const uint32_t* s_off;   // clamped to T
     const int32_t* s_ids;
+    const int32_t* s_order;  // experts, those of most stages first; nullptr: as they are numbered
     int64_t lda, ldb;
     Items items;
     int grid, mband;
@@ -91,8 +93,12 @@ struct WeightsJob {
 
     __device__ __forceinline__ void locate(int W, Coord& c) const {
         const bool split = W >= items.full;
-        const int L = split ? items.full + (W - items.full) / 2 : W, tiles = p.ntn * p.ntk;
-        const int e = (int)((uint32_t)L / (uint32_t)tiles), local = L - e * tiles;
+        int L = split ? items.full + (W - items.full) / 2 : W;
+        // every other whole round runs backwards, so that what falls along the list is even over the workgroups
+        const int round = (int)((uint32_t)L / (uint32_t)grid);
+        if ((round & 1) && (round + 1) * grid <= items.full) L = (2 * round + 1) * grid - 1 - L;
+        const int tiles = p.ntn * p.ntk, turn = (int)((uint32_t)L / (uint32_t)tiles), local = L - turn * tiles;
+        const int e = s_order ? s_order[turn] : turn;
         const int mb = mband < p.ntn ? mband : p.ntn;  // bands of mband tiles along N, K walked within one
         const int band = (int)((uint32_t)local / (uint32_t)(mb * p.ntk)), r = local - band * mb * p.ntk;
         const int left = p.ntn - band * mb, gm = left < mb ? left : mb, kt = (int)((uint32_t)r / (uint32_t)gm);
@@ -114,6 +120,14 @@ struct WeightsJob {
             if (c.cols_in > 0) return true;
         }
         return false;
+    }
+    // dbias: the sums of dc's columns, by one tile of a row of tiles, another in each row (they take
+    // longer: the same workgroups would get all of a band's first ones)
+    __device__ __forceinline__ bool sums(const Coord& c) const { return c.k0 == c.n0 / TL::BM % p.ntk * TL::BN; }
+    __device__ __forceinline__ void put_sum(const Coord& c, int row, float v) const {
+        if (p.accumulate && c.stages == 0) return;
+        float* at = p.dbias + (int64_t)c.e * p.N + c.n0 + row;
+        *at = p.accumulate ? *at + v : v;
     }
     template <class>
     __device__ __forceinline__ void finish(const Coord& c, const v4f (&acc)[TL::TN][TL::TM], int wm, int wn,
@@ -137,27 +151,50 @@ __device__ __forceinline__ void load_groups(const WeightsArgs& p, uint32_t* s_of
     __syncthreads();
 }
 
-template <class TL>
+// Experts by falling number of stages (ties to the lower id).  The tiles of a launch are dealt out in
+// rounds, to and fro: in this order the workgroups' shares differ by less than a long tile
+// (32768 rows of 64 uneven experts, 1536 x 4096: as numbered 793 us).
+__device__ __forceinline__ void order_experts(const WeightsArgs& p, const uint32_t* s_off, const int32_t* s_ids,
+                                              uint32_t* s_cost, int32_t* s_order) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_cost[e] = 0;
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.G; g += blockDim.x)
+        if (s_ids[g] >= 0 && s_ids[g] < p.E && s_off[g] < s_off[g + 1])
+            atomicAdd(&s_cost[s_ids[g]], (s_off[g + 1] - s_off[g] + kStageDepth - 1) / kStageDepth);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        const uint32_t mine = s_cost[e];
+        int rank = 0;
+        for (int o = 0; o < p.E; ++o) rank += s_cost[o] > mine || (s_cost[o] == mine && o < e);
+        s_order[rank] = e;
+    }
+    __syncthreads();
+}
+
+template <class TL, bool BIAS>
 __global__ __launch_bounds__(TL::kThreads, 1) void weights_kernel(const WeightsArgs p) {
     __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
     __shared__ uint32_t s_off[kMaxGroups + 1];
-    __shared__ int32_t s_ids[kMaxGroups];
+    __shared__ int32_t s_ids[kMaxGroups], s_order[kMaxGroups];
     load_groups(p, s_off, s_ids);
+    const bool sorted = p.E <= kMaxGroups;
+    static_assert(TL::kLds >= 4 * kMaxGroups, "the costs fit the ring");
+    if (sorted) order_experts(p, s_off, s_ids, reinterpret_cast<uint32_t*>(s_ring), s_order);
     const int grid = (int)gridDim.x;
-    WeightsJob<TL> job{p, s_off, s_ids, p.N * 2, p.K * 2, items_of(p.E * p.ntn * p.ntk, grid), grid, 4};
+    WeightsJob<TL, BIAS> job{p, s_off, s_ids, sorted ? s_order : nullptr, p.N * 2, p.K * 2, items_of(p.E * p.ntn * p.ntk, grid), grid, 4};
     run_tiles<TL>(job, s_ring, gemm::xcd_remap((int)blockIdx.x, grid), grid);
 }
 
 // Small tiles, one a workgroup, their depth split over its waves.
-template <class TL>
+template <class TL, bool BIAS>
 __global__ __launch_bounds__(TL::kThreads, 1) void weights_split_kernel(const WeightsArgs p) {
     __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
     __shared__ uint32_t s_off[kMaxGroups + 1];
     __shared__ int32_t s_ids[kMaxGroups];
     load_groups(p, s_off, s_ids);
     const int items = p.E * p.ntn * p.ntk;
-    WeightsJob<TL> job{p, s_off, s_ids, p.N * 2, p.K * 2, {items, items}, 1, 4};
-    typename WeightsJob<TL>::Coord c;
+    WeightsJob<TL, BIAS> job{p, s_off, s_ids, nullptr, p.N * 2, p.K * 2, {items, items}, items, 4};
+    typename WeightsJob<TL, BIAS>::Coord c;
     job.locate(gemm::xcd_remap((int)blockIdx.x, (int)gridDim.x), c);
     if (p.accumulate && c.stages == 0) return;
     run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
@@ -165,43 +202,6 @@ __global__ __launch_bounds__(TL::kThreads, 1) void weights_split_kernel(const We
         fetch(p, c.e, c.n0 + row, c.k0 + col, old);
         write(p, c.e, c.n0 + row, c.k0 + col, v, old);
     });
-}
-
-// dbias: 64 columns of one expert a workgroup, its rows over 16 waves of 8 rows each.
-constexpr int kBiasWaves = 16;
-__global__ __launch_bounds__(kBiasWaves * kWave) void bias_kernel(const WeightsArgs p) {
-    __shared__ float s[kBiasWaves][8][64];
-    const int e = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t n = (int64_t)blockIdx.x * 64 + (lane % 8) * 8;
-    float sum[8] = {};
-    bool any = false;
-    for (int g = 0; g < p.G; ++g) {
-        if (expert_of(p.ids, g) != e) continue;
-        const GroupRange r = rows_of(p.off, p.ids, g, p.T, p.E);
-        any = any || r.lo < r.hi;
-#pragma unroll 4
-        for (int64_t t = r.lo + wave * 8 + lane / 8; t < r.hi; t += kBiasWaves * 8)
-            if (n < p.N) {
-                float v[8];
-                unpack8(*reinterpret_cast<const uint4*>(p.dc + (t * p.N + n) * 2), v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] += v[i];
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[wave][lane / 8][(lane % 8) * 8 + i] = sum[i];
-    __syncthreads();
-    if (wave == 0) {
-        float v = 0.0f;
-        for (int w = 0; w < kBiasWaves; ++w)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v += s[w][i][lane];
-        const int64_t at = (int64_t)blockIdx.x * 64 + lane;
-        if (at < p.N) {
-            float* d = p.dbias + (int64_t)e * p.N + at;
-            *d = p.accumulate ? *d + v : v;
-        }
-    }
 }
 
 int64_t compute_units() {
@@ -223,26 +223,26 @@ hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, b
     };
     const char* f = getenv("MXG_BF16_WTILE");
     const int t = f ? atoi(f) : 256;
-    if (t == 64) {
-        using TL = SplitTile<64, 64, 4, true, true>;
-        const int64_t n = tiles(64, 64);
-        hipLaunchKernelGGL(weights_split_kernel<TL>, dim3((unsigned)n), dim3(TL::kThreads), 0, stream, p);
-    } else if (t == 32) {
-        using TL = SplitTile<64, 32, 5, true, true>;
-        const int64_t n = tiles(64, 32);
-        hipLaunchKernelGGL(weights_split_kernel<TL>, dim3((unsigned)n), dim3(TL::kThreads), 0, stream, p);
-    } else if (t == 128) {
-        using TL = Tile<128, 128, 2, 2, true, true>;
-        const int64_t n = tiles(128, 128), room = compute_units() * 2;
-        hipLaunchKernelGGL(weights_kernel<TL>, dim3((unsigned)(n < room ? n : room)), dim3(TL::kThreads), 0, stream, p);
-    } else {
-        using TL = Tile<256, 256, 4, 2, true, true>;
-        const int64_t n = tiles(256, 256), room = compute_units();
-        hipLaunchKernelGGL(weights_kernel<TL>, dim3((unsigned)(n < room ? n : room)), dim3(TL::kThreads), 0, stream, p);
-    }
-    if (dbias)
-        hipLaunchKernelGGL(bias_kernel, dim3((unsigned)((N + 63) / 64), (unsigned)E), dim3(kBiasWaves * kWave), 0,
+    auto split = [&](auto tile, auto bias) {
+        using TL = decltype(tile);
+        const int64_t n = tiles(TL::BM, TL::BN);
+        hipLaunchKernelGGL((weights_split_kernel<TL, decltype(bias)::value>), dim3((unsigned)n), dim3(TL::kThreads), 0,
                            stream, p);
+    };
+    auto whole = [&](auto tile, auto bias, int per_cu) {
+        using TL = decltype(tile);
+        const int64_t n = tiles(TL::BM, TL::BN), room = compute_units() * per_cu;
+        hipLaunchKernelGGL((weights_kernel<TL, decltype(bias)::value>), dim3((unsigned)(n < room ? n : room)),
+                           dim3(TL::kThreads), 0, stream, p);
+    };
+    auto pick = [&](auto bias) {
+        if (t == 64) split(SplitTile<64, 64, 4, true, true>{}, bias);
+        else if (t == 32) split(SplitTile<64, 32, 5, true, true>{}, bias);
+        else if (t == 128) whole(Tile<128, 128, 2, 2, true, true>{}, bias, 2);
+        else whole(Tile<256, 256, 4, 2, true, true>{}, bias, 1);
+    };
+    if (dbias) pick(std::true_type{});
+    else pick(std::false_type{});
     return hipGetLastError();
 }
 
