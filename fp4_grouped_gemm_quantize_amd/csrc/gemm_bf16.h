@@ -16,6 +16,50 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 enum Act { kNone = 0, kRelu = 1, kGelu = 2, kSilu = 3, kSwiglu = 4 };  // mxg_activation
 
+// ---------------------------------------------------------------------------
+// Host side: which kernel a product of given sizes runs, by the time that each would take.
+// A launch of n tiles runs in rounds of `per_cu` workgroups a CU; a round takes `base` us and,
+// for each 64 of the depth that a wave has before it, `stage` us or what the workgroups'
+// operands take at `rate` bytes a ns (TB/s) from the near caches, whichever is more.  Fitted to
+// the times beside the candidates, of which it picks the first or one within 15 % of it (the
+// sizes' own minimum, the weights from HBM, is the same for all).
+struct Candidate {
+    int rows, cols, waves, per_cu;  // of a tile; waves its depth is split over
+    double base, stage, rate;
+};
+struct Work {
+    int64_t groups, rows;  // that own output rows, and how many in all
+    int64_t cols, depth;   // of the output, and of the sum
+};
+inline double time_of(const Candidate& c, const Work& w, int64_t cus) {
+    // the host does not see the group sizes: whole tiles, and half a tile more for each group
+    const int64_t half = (2 * w.rows + w.groups * c.rows) / (2 * c.rows);
+    const int64_t mt = w.groups == 1 ? (w.rows + c.rows - 1) / c.rows : half > w.groups ? half : w.groups;
+    const int64_t nt = (w.cols + c.cols - 1) / c.cols, room = cus * c.per_cu;
+    const int64_t stages = (w.depth + 63) / 64, mine = (stages + c.waves - 1) / c.waves;
+    // rows and columns past the output's are not loaded
+    const double tile = (double)w.rows / (double)mt + (double)w.cols / (double)nt;
+    auto round = [&](double n) {
+        const double near = (double)stages * tile * 128.0 * n / c.rate * 1e-6, far = (double)mine * c.stage;
+        return n > 0 ? c.base + (near > far ? near : far) : 0.0;
+    };
+    const double tiles = (double)mt * (double)nt, whole = (double)(int64_t)(tiles / (double)room);
+    return whole * round((double)room) + round(tiles - whole * (double)room);
+}
+template <int N>
+inline int fastest(const Candidate (&c)[N], const Work& w, int64_t cus) {
+    int best = 0;
+    double least = time_of(c[0], w, cus);
+    for (int i = 1; i < N; ++i) {
+        const double t = time_of(c[i], w, cus);
+        if (t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    return best;
+}
+
 // The group's rows; without routing one group of all rows.
 __device__ __forceinline__ GroupRange rows_of(const uint32_t* off, const int32_t* ids, int g, int64_t T, int E) {
     if (off == nullptr) return {0, T};

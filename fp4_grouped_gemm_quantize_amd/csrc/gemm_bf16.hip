@@ -1,8 +1,6 @@
 // gemm_bf16.hip -- ragged grouped product of BF16 operands with bias, activation and
 // residual in its epilogue, the gradient of its rows through the activation before
 // them, and the activation's gradient by itself, for gfx950.
-#include <stdlib.h>
-
 #include "gemm_bf16_tile.h"
 
 namespace mxg {
@@ -216,21 +214,35 @@ hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Measured (us a call; 256 / 128 / 32 rows in the ring kernel, 64 / 32 / 16 with the depth split):
+// dense 8192 x 8192 of 8192: 750 / 1390 / - / -; 2048 x 2048 of 2048: 45 / 43 / 56 / 57 / 108 / 160;
+// 1024 x 1024 of 1024: 27 / 14 / 10 / 13 / 20 / 34; 256 x 4096 of 4096: 80 / 37 / 29 / 29 / 38 / 58;
+// 128 x 4096 of 7168: 105 / 59 / 42 / 25 / 38 / 49; 16 x 4096 of 7168: 101 / 55 / 41 / 20 / 13 / 19;
+// 1 x 4096 of 4096: 60 / 33 / 24 / 13 / 8.3 / 7.1; 64 x 64 of 7168: 104 / 58 / 34 / 20 / 12 / 9.3;
+// 8192 x 64 of 7168: 132 / 58 / 42 / 26 / 47 / 54; 5003 rows of 24 uneven groups, 2080 x 1000: 54 / 53 / 71 /
+// 83 / 172 / 253; the rows' gradient of 8192 x 7168 of 64: 38 / 56 / 85 / 203 / 600 / 1235.
+constexpr Candidate kRowTiles[] = {
+    {256, 256, 1, 1, 5.0, 1.1, 12.0}, {128, 128, 1, 2, 4.0, 0.6, 11.0}, {32, 128, 1, 3, 4.0, 0.37, 11.0},
+    {64, 64, 4, 1, 3.0, 0.7, 7.5},    {32, 32, 4, 1, 3.0, 0.33, 7.5},   {16, 32, 8, 1, 4.0, 0.37, 7.5},
+};
+
+int row_tile(const Bf16Problem& p, bool back) {
+    const int64_t hint = p.max_rows_hint < p.T ? (p.max_rows_hint > 0 ? p.max_rows_hint : 1) : p.T;
+    int64_t groups = p.G < p.T ? p.G : p.T;
+    if (groups > 1 + p.T - hint) groups = 1 + p.T - hint;  // the rows beside the largest group's
+    return fastest(kRowTiles, {groups, p.T, back ? p.K : p.N, back ? p.N : p.K}, compute_units());
+}
+
 template <bool BACK>
 hipError_t launch(const Bf16Problem& p, hipStream_t stream) {
-    using Large = Tile<256, 256, 4, 2, false, BACK>;
-    using Mid = Tile<128, 128, 2, 2, false, BACK>;
-    using Small = Tile<32, 128, 1, 4, false, BACK>;
-    const char* f = getenv("MXG_BF16_TILE");
-    const int t = f ? atoi(f) : 256;
-    if (t == 128) return launch_tile<Mid, BACK>(p, 2, 4, stream);
-    if (t == 32) return launch_tile<Small, BACK>(p, 3, 1 << 30, stream);
-    if (t == 6464) return launch_split<SplitTile<64, 64, 4, false, BACK>, BACK>(p, stream);
-    if (t == 6432) return launch_split<SplitTile<64, 32, 5, false, BACK>, BACK>(p, stream);
-    if (t == 3232) return launch_split<SplitTile<32, 32, 8, false, BACK>, BACK>(p, stream);
-    if (t == 1632) return launch_split<SplitTile<16, 32, 8, false, BACK>, BACK>(p, stream);
-    if (t == 1664) return launch_split<SplitTile<16, 64, 6, false, BACK>, BACK>(p, stream);
-    return launch_tile<Large, BACK>(p, 1, 4, stream);
+    switch (row_tile(p, BACK)) {
+        case 0: return launch_tile<Tile<256, 256, 4, 2, false, BACK>, BACK>(p, 1, 4, stream);
+        case 1: return launch_tile<Tile<128, 128, 2, 2, false, BACK>, BACK>(p, 2, 4, stream);
+        case 2: return launch_tile<Tile<32, 128, 1, 4, false, BACK>, BACK>(p, 3, 1 << 20, stream);
+        case 3: return launch_split<SplitTile<64, 64, 4, 2, false, BACK>, BACK>(p, stream);
+        case 4: return launch_split<SplitTile<32, 32, 4, 4, false, BACK>, BACK>(p, stream);
+        default: return launch_split<SplitTile<16, 32, 8, 3, false, BACK>, BACK>(p, stream);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -256,6 +268,7 @@ __global__ __launch_bounds__(256) void activation_backward_kernel(const void* dc
 
 }  // namespace
 
+int bf16_tile_choice(const Bf16Problem& p, bool back) { return kRowTiles[row_tile(p, back)].rows; }
 hipError_t launch_matmul_bf16(const Bf16Problem& p, hipStream_t stream) { return launch<false>(p, stream); }
 hipError_t launch_matmul_bf16_backward(const Bf16Problem& p, hipStream_t stream) { return launch<true>(p, stream); }
 

@@ -504,17 +504,17 @@ __device__ __forceinline__ void put_blocks(const v4f (&acc)[TL::TN][TL::TM], int
 
 // ---------------------------------------------------------------------------
 // Few tiles, or few rows: a small tile's depth is split over the waves of its workgroup.
-// Each wave takes every WAVES-th stage through two slots of its own, without a barrier,
+// Each wave takes every WAVES-th stage through SLOTS slots of its own, without a barrier,
 // and holds the whole tile; the waves' sums are joined in LDS in wave order.
-template <int BM_, int BN_, int WAVES_, bool AWIDE_, bool BWIDE_>
+template <int BM_, int BN_, int WAVES_, int SLOTS_, bool AWIDE_, bool BWIDE_>
 struct SplitTile {
-    static constexpr int BM = BM_, BN = BN_, kWaves = WAVES_, kThreads = kWave * kWaves;
+    static constexpr int BM = BM_, BN = BN_, kWaves = WAVES_, kThreads = kWave * kWaves, kSlots = SLOTS_;
     static constexpr int TM = BM / 16, TN = BN / 16;
     using A = Operand<BM, AWIDE_, 1>;
     using B = Operand<BN, BWIDE_, 1>;
     static constexpr int kStage = A::kBytes + B::kBytes, kLoads = A::kLoads + B::kLoads;
     static constexpr int kPitch = BN + 4;  // floats a row of a wave's sums
-    static constexpr int kRing = kWaves * 2 * kStage, kSums = kWaves * BM * kPitch * 4;
+    static constexpr int kRing = kWaves * kSlots * kStage, kSums = kWaves * BM * kPitch * 4;
     static constexpr int kLds = kRing > kSums ? kRing : kSums;
 };
 
@@ -526,11 +526,11 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
     using B = typename TL::B;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t ring0 = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * 2 * TL::kStage);
+    const uint32_t ring0 = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * TL::kSlots * TL::kStage);
 
     // this wave's stages: `mine` of them; the producer is at depth `at` of segment c
     const int mine = c.stages > wave ? (c.stages - wave + TL::kWaves - 1) / TL::kWaves : 0;
-    int at = wave * kStageDepth, issued = 0;
+    int at = wave * kStageDepth, issued = 0, slot_in = 0, slot_out = 0;
     const int64_t sa = A::step(job.lda) / kStageDepth, sb = B::step(job.ldb) / kStageDepth;  // bytes a unit of depth
     const uint32_t lda = (uint32_t)job.lda, ldb = (uint32_t)job.ldb;
     A fa;
@@ -552,13 +552,14 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
         const int rb = __builtin_amdgcn_readfirstlane(more ? B::range(c.cols_in, left, c.depth, ldb) : 0);
         const v4i da = {(int)(uint32_t)pa, (int)(uint32_t)(pa >> 32), ra, 0x00020000};
         const v4i db = {(int)(uint32_t)pb, (int)(uint32_t)(pb >> 32), rb, 0x00020000};
-        const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(ring0 + (issued & 1) * TL::kStage);
+        const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(ring0 + slot_in * TL::kStage);
         __asm__ volatile("s_nop 4");  // wait states of what the lane reads wrote
 #pragma unroll
         for (int l = 0; l < A::kLoads; ++l) fa.load(da, l, lda, slot);
 #pragma unroll
         for (int l = 0; l < B::kLoads; ++l) fb.load(db, l, ldb, slot + A::kBytes);
         ++issued;
+        slot_in = slot_in + 1 < TL::kSlots ? slot_in + 1 : 0;
         at += TL::kWaves * kStageDepth;
     };
     const uint32_t abase = A::lane_base(lane, 0), bbase = B::lane_base(lane, 0);
@@ -570,11 +571,12 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
     float sum[Job::kSums ? TM : 1] = {};
     bool add_up = false;
     if constexpr (Job::kSums) add_up = job.sums(c);
-    load();
-    load();
+#pragma unroll
+    for (int s = 0; s < TL::kSlots; ++s) load();
     for (int s = 0; s < mine; ++s) {
-        const uint32_t ca = ring0 + (s & 1) * TL::kStage + abase, cb = ca - abase + A::kBytes + bbase;
-        gemm::wait_vmem<TL::kLoads>();
+        const uint32_t ca = ring0 + slot_out * TL::kStage + abase, cb = ca - abase + A::kBytes + bbase;
+        slot_out = slot_out + 1 < TL::kSlots ? slot_out + 1 : 0;
+        gemm::wait_vmem<(TL::kSlots - 1) * TL::kLoads>();
         __asm__ volatile("" ::: "memory");
         v8b tf[2][TM], nf[2][TN];
 #pragma unroll

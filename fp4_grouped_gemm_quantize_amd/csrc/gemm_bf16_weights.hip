@@ -5,8 +5,6 @@
 // depth is their row index), so both go through the transposing LDS loads.  A tile's depth
 // is its expert's rows, group by group; the tiles of all experts are one list, so that short
 // and long ones share the chip, and a tile without rows costs its zeros alone.
-#include <stdlib.h>
-
 #include "gemm_bf16_tile.h"
 
 namespace mxg {
@@ -209,7 +207,40 @@ int64_t compute_units() {
     return cus > 0 ? cus : 256;
 }
 
+// Measured (us a call; 256 and 128 rows in the ring kernel, 64 x 64 and 64 x 32 with the depth split):
+// 32768 rows of 64 uneven experts, 1536 x 4096: 690 / 1220 / 2590 / 4480; 8192 rows, 4096 x 7168: 420 / 610 / 766 /
+// 1314; 16384 rows of 8, 256 x 2048: 60 / 40 / 42 / 67; 4096 rows, 512 x 1024: 98 / 50 / 18 / 17; 8192 rows,
+// 64 x 7168: 155 / 98 / 34 / 31; 5003 rows of 24, 1000 x 2080: 91 / 127 / 283 / 469.
+constexpr Candidate kWeightTiles[] = {
+    {256, 256, 1, 1, 12.0, 1.1, 12.0}, {128, 128, 1, 2, 6.0, 0.6, 11.0}, {64, 64, 4, 1, 3.0, 0.95, 11.0},
+    {64, 32, 4, 1, 3.0, 0.87, 11.0},
+};
+
+int weight_tile(int G, int E, int64_t T, int64_t N, int64_t K) {
+    // each expert is a product of its own, of T / E rows' depth where every one has some
+    int64_t used = G < T ? G : T;
+    used = used < E ? (used > 0 ? used : 1) : E;
+    // (the tiles of all experts as one output of N rows each: whole tiles, no half ones)
+    int best = 0;
+    double least = 0.0;
+    const int n = sizeof kWeightTiles / sizeof kWeightTiles[0];
+    for (int i = 0; i < n; ++i) {
+        const Candidate& c = kWeightTiles[i];
+        const int64_t rows = (N + c.rows - 1) / c.rows * c.rows * used;
+        const double t = time_of(c, {1, rows, K, T / used}, compute_units());
+        if (i == 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    return best;
+}
+
 }  // namespace
+
+int bf16_weights_tile_choice(int G, int E, int64_t T, int64_t N, int64_t K) {
+    return kWeightTiles[weight_tile(G, E, T, N, K)].rows;
+}
 
 hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, bool dw32, float* dbias,
                                       bool accumulate, const uint32_t* off, const int32_t* ids, int G, int E,
@@ -221,29 +252,31 @@ hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, b
         p.ntk = (int)((K + BN - 1) / BN);
         return (int64_t)E * p.ntn * p.ntk;
     };
-    const char* f = getenv("MXG_BF16_WTILE");
-    const int t = f ? atoi(f) : 256;
     auto split = [&](auto tile, auto bias) {
         using TL = decltype(tile);
         const int64_t n = tiles(TL::BM, TL::BN);
+        if (n > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
         hipLaunchKernelGGL((weights_split_kernel<TL, decltype(bias)::value>), dim3((unsigned)n), dim3(TL::kThreads), 0,
                            stream, p);
+        return hipGetLastError();
     };
     auto whole = [&](auto tile, auto bias, int per_cu) {
         using TL = decltype(tile);
         const int64_t n = tiles(TL::BM, TL::BN), room = compute_units() * per_cu;
+        if (2 * n > INT32_MAX) return hipErrorInvalidValue;
         hipLaunchKernelGGL((weights_kernel<TL, decltype(bias)::value>), dim3((unsigned)(n < room ? n : room)),
                            dim3(TL::kThreads), 0, stream, p);
+        return hipGetLastError();
     };
     auto pick = [&](auto bias) {
-        if (t == 64) split(SplitTile<64, 64, 4, true, true>{}, bias);
-        else if (t == 32) split(SplitTile<64, 32, 5, true, true>{}, bias);
-        else if (t == 128) whole(Tile<128, 128, 2, 2, true, true>{}, bias, 2);
-        else whole(Tile<256, 256, 4, 2, true, true>{}, bias, 1);
+        switch (weight_tile(G, E, T, N, K)) {
+            case 0: return whole(Tile<256, 256, 4, 2, true, true>{}, bias, 1);
+            case 1: return whole(Tile<128, 128, 2, 2, true, true>{}, bias, 2);
+            case 2: return split(SplitTile<64, 64, 4, 2, true, true>{}, bias);
+            default: return split(SplitTile<64, 32, 4, 3, true, true>{}, bias);
+        }
     };
-    if (dbias) pick(std::true_type{});
-    else pick(std::false_type{});
-    return hipGetLastError();
+    return dbias ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace mxg
