@@ -41,6 +41,7 @@ FORMATS = {FP8_ROWWISE: "fp8_e4m3_rowwise", MXFP8: "mxfp8_e4m3", MXFP4: "mxfp4_e
 F32, BF16 = 0, 1                       # mxg_dtype
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1    # mxg_score
 NORM_PLAIN, NORM_FP8_ROWWISE, NORM_MXFP8, NORM_FP8_BLOCK128 = 0, 1, 2, 3   # mxg_norm_format
+BF16_FORWARD, BF16_BACKWARD, BF16_BACKWARD_WEIGHTS = 0, 1, 2                # mxg_bf16_product
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU, ACT_SWIGLU = 0, 1, 2, 3, 4         # mxg_activation
 
 SUCCESS, ERROR_INVALID_VALUE, ERROR_NOT_SUPPORTED, ERROR_LAUNCH = 0, 1, 2, 3
@@ -62,7 +63,7 @@ EXPORTED = ("mx_grouped_quantize", "mx_grouped_quantize_gather", "mx_grouped_qua
             "mx_rmsnorm_workspace_bytes", "mx_rmsnorm_backward", "mx_grouped_matmul_bf16",
             "mx_grouped_matmul_bf16_backward", "mx_grouped_matmul_bf16_backward_weights", "mx_activation_backward",
             "mxg_clock_probe",
-            "mxg_fp8_tile", "mxg_block128_tile", "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
+            "mxg_fp8_tile", "mxg_block128_tile", "mxg_bf16_tile", "mxg_validation_message", "mxg_routing_violation", "mxg_status_string")
 
 
 class MxgError(RuntimeError):
@@ -162,6 +163,8 @@ def lib() -> ctypes.CDLL:
         L.mxg_fp8_tile.restype = ctypes.c_int32
         L.mxg_block128_tile.argtypes = [_I32, _I64, _I64, _I64, _I64]
         L.mxg_block128_tile.restype = ctypes.c_int32
+        L.mxg_bf16_tile.argtypes = [ctypes.c_int, _I32, _I32, _I64, _I64, _I64, _I64]
+        L.mxg_bf16_tile.restype = ctypes.c_int32
         L.mxg_status_string.argtypes = [ctypes.c_int]
         L.mxg_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -1002,6 +1005,15 @@ def block128_tile(num_groups: int, total_rows: int, N: int, K: int, max_rows_per
     return int(lib().mxg_block128_tile(int(num_groups), int(total_rows), int(N), int(K), int(max_rows_per_group_hint)))
 
 
+def bf16_tile(product: int, num_groups: int, num_experts: int, total_rows: int, N: int, K: int,
+              max_rows_per_group_hint: int = 0):
+    """(rows, columns) of a tile of the kernel that a BF16 product of these sizes (BF16_FORWARD), its rows'
+    gradient (BF16_BACKWARD) or its weights' (BF16_BACKWARD_WEIGHTS) runs; (0, 0): nothing, or refused."""
+    t = lib().mxg_bf16_tile(product, int(num_groups), int(num_experts), int(total_rows), int(N), int(K),
+                            int(max_rows_per_group_hint))
+    return divmod(t, 1000)
+
+
 def mx_silu_quantize_block128(h, y_q, y_scales, row_offsets) -> None:
     """SwiGLU of bf16 h [T, 2I] (gate/up interleaved by column), requantized from fp32 to e4m3
     y_q u8 [T, I] with an fp32 scale per 1 x 128 block in y_scales [T, ceil(I/128)]."""
@@ -1047,24 +1059,6 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
-def _span(t):
-    a = t.data_ptr()
-    return a, a + t.nbytes
-
-
-def _outputs_apart(outputs, inputs) -> None:
-    """Refuse outputs that share memory with an input or another output; both are lists of (name, tensor or None)."""
-    seen = [(n, *_span(t)) for n, t in inputs if t is not None]
-    for name, t in outputs:
-        if t is None:
-            continue
-        lo, hi = _span(t)
-        for other, a, b in seen:
-            if lo < b and a < hi:
-                raise ValueError(f"{name} and {other} may not overlap")
-        seen.append((name, lo, hi))
-
-
 def _type(t) -> int:
     return F32 if t.dtype == torch.float32 else BF16
 
@@ -1093,16 +1087,6 @@ def mx_rmsnorm(x, weight, residual=None, h=None, y=None, form: int = NORM_PLAIN,
                 (S,) if form == NORM_FP8_ROWWISE else (S, H // 32 if form == NORM_MXFP8 else _blocks128(H)), dev)
     elif y is None:
         raise ValueError("give y, or q with scales, or all three")
-    # h may be its residual or, both bf16, x
-    at = None if h is None else h.data_ptr()
-    reads = [("weight", weight)]
-    if at is None or at != x.data_ptr() or h.dtype != x.dtype:
-        reads.append(("x", x))
-    if residual is not None and at != residual.data_ptr():
-        reads.append(("residual", residual))
-    _outputs_apart((("h", h),), reads)
-    _outputs_apart((("y", y), ("q", q), ("scales", scales)), (("weight", weight), ("x", x), ("residual", residual),
-                                                               ("h", h)))
     _run("mx_rmsnorm", dev, form, _type(x if residual is None else residual), x.data_ptr(), _opt(residual),
          _type(weight), weight.data_ptr(), weight_offset, eps, S, H, _opt(h), _opt(y), _opt(q), _opt(scales))
 
@@ -1140,12 +1124,6 @@ def mx_rmsnorm_backward(dy, h, weight, dx=None, dh=None, dx_bf16=None, dweight=N
         raise ValueError("give dx, dx_bf16 or dweight")
     else:
         workspace = None
-    apart = (("dx_bf16", dx_bf16), ("dweight", dweight), ("workspace", workspace))
-    reads = (("dy", dy), ("h", h), ("weight", weight))
-    if dx is not None and dh is not None and dx.data_ptr() == dh.data_ptr():
-        _outputs_apart((("dx", dx), *apart), reads)
-    else:
-        _outputs_apart((("dx", dx), *apart), (*reads, ("dh", dh)))
     _run("mx_rmsnorm_backward", dev, _type(h), dy.data_ptr(), h.data_ptr(), _type(weight), weight.data_ptr(),
          weight_offset, eps, _opt(dh), S, H, _opt(dx), _opt(dx_bf16), _opt(dweight), _opt(workspace))
 
@@ -1188,8 +1166,6 @@ def mx_grouped_matmul_bf16(a, b, c, row_offsets=None, expert_ids=None, bias=None
     if z is not None:
         _expect(z, "z", _BF16, (T, N), dev)
     G = _bf16_groups(row_offsets, expert_ids, dev)
-    own = residual is not None and residual.data_ptr() == c.data_ptr()
-    _outputs_apart((("c", c), ("z", z)), (("a", a), ("b", b), ("bias", bias), ("residual", None if own else residual)))
     _run("mx_grouped_matmul_bf16", dev, act, a.data_ptr(), b.data_ptr(), _opt(bias), _opt(residual), _type(c),
          c.data_ptr(), _opt(z), _opt(row_offsets), _opt(expert_ids), G, E, T, N, K, int(max_rows_per_group_hint))
 
@@ -1210,8 +1186,6 @@ def mx_grouped_matmul_bf16_backward(dc, b, da, row_offsets=None, expert_ids=None
     if z is not None:
         _expect(z, "z", _BF16, (T, wide), dev)
     G = _bf16_groups(row_offsets, expert_ids, dev)
-    own = z is not None and z.data_ptr() == da.data_ptr()
-    _outputs_apart((("da", da),), (("dc", dc), ("b", b), ("z", None if own else z)))
     _run("mx_grouped_matmul_bf16_backward", dev, act, dc.data_ptr(), b.data_ptr(), _opt(z), da.data_ptr(),
          _opt(row_offsets), _opt(expert_ids), G, E, T, N, K, int(max_rows_per_group_hint))
 
@@ -1233,7 +1207,6 @@ def mx_grouped_matmul_bf16_backward_weights(dc, a, dw, row_offsets=None, expert_
     if dbias is not None:
         _expect(dbias, "dbias", _F32, (E, N), dev)
     G = _bf16_groups(row_offsets, expert_ids, dev)
-    _outputs_apart((("dw", dw), ("dbias", dbias)), (("dc", dc), ("a", a)))
     _run("mx_grouped_matmul_bf16_backward_weights", dev, dc.data_ptr(), a.data_ptr(), _type(dw), dw.data_ptr(),
          _opt(dbias), 1 if accumulate else 0, _opt(row_offsets), _opt(expert_ids), G, E, T, N, K)
 
@@ -1246,9 +1219,6 @@ def mx_activation_backward(act: int, dc, z, dz) -> None:
     wide = 2 * N if act == ACT_SWIGLU else N
     _expect(z, "z", _BF16, (T, wide), dev)
     _expect(dz, "dz", _BF16, (T, wide), dev)
-    at = dz.data_ptr()
-    _outputs_apart((("dz", dz),), (("z", None if at == z.data_ptr() else z),
-                                   ("dc", None if at == dc.data_ptr() and act != ACT_SWIGLU else dc)))
     _run("mx_activation_backward", dev, act, dc.data_ptr(), z.data_ptr(), dz.data_ptr(), T, N)
 
 

@@ -268,7 +268,10 @@ __global__ __launch_bounds__(256) void activation_backward_kernel(const void* dc
 
 }  // namespace
 
-int bf16_tile_choice(const Bf16Problem& p, bool back) { return kRowTiles[row_tile(p, back)].rows; }
+int bf16_tile_choice(const Bf16Problem& p, bool back) {
+    const Candidate& c = kRowTiles[row_tile(p, back)];
+    return 1000 * c.rows + c.cols;
+}
 hipError_t launch_matmul_bf16(const Bf16Problem& p, hipStream_t stream) { return launch<false>(p, stream); }
 hipError_t launch_matmul_bf16_backward(const Bf16Problem& p, hipStream_t stream) { return launch<true>(p, stream); }
 

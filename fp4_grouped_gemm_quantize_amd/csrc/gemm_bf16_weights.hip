@@ -217,10 +217,10 @@ constexpr Candidate kWeightTiles[] = {
 };
 
 int weight_tile(int G, int E, int64_t T, int64_t N, int64_t K) {
-    // each expert is a product of its own, of T / E rows' depth where every one has some
+    // The experts that may have rows, as one output: N rows each, filled up to whole tiles, and a depth
+    // of their share of the rows.
     int64_t used = G < T ? G : T;
     used = used < E ? (used > 0 ? used : 1) : E;
-    // (the tiles of all experts as one output of N rows each: whole tiles, no half ones)
     int best = 0;
     double least = 0.0;
     const int n = sizeof kWeightTiles / sizeof kWeightTiles[0];
@@ -239,7 +239,8 @@ int weight_tile(int G, int E, int64_t T, int64_t N, int64_t K) {
 }  // namespace
 
 int bf16_weights_tile_choice(int G, int E, int64_t T, int64_t N, int64_t K) {
-    return kWeightTiles[weight_tile(G, E, T, N, K)].rows;
+    const Candidate& c = kWeightTiles[weight_tile(G, E, T, N, K)];
+    return 1000 * c.rows + c.cols;
 }
 
 hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, bool dw32, float* dbias,

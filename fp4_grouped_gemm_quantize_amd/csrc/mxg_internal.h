@@ -151,7 +151,7 @@ hipError_t launch_matmul_bf16_backward(const Bf16Problem& p, hipStream_t stream)
 hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, bool dw32, float* dbias,
                                       bool accumulate, const uint32_t* off, const int32_t* ids, int G, int E,
                                       int64_t T, int64_t N, int64_t K, hipStream_t stream);
-// Rows of a tile of the kernel that a product, its rows' gradient (back) or its weights' gradient of these sizes runs.
+// 1000 * rows + columns of a tile of the kernel that a product, its rows' gradient (back) or its weights' gradient of these sizes runs.
 int bf16_tile_choice(const Bf16Problem& p, bool back);
 int bf16_weights_tile_choice(int G, int E, int64_t T, int64_t N, int64_t K);
 hipError_t launch_activation_backward(int act, const void* dc, const void* z, void* dz, int64_t T, int64_t N,

@@ -79,8 +79,8 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
     return v;
 }
 
-// Sum and maximum over the workgroup, in a fixed order; s holds a word per wave and is
-// used again only after another barrier.
+// Sum over the workgroup, in a fixed order; s holds a word per wave and is used again only
+// after another barrier.
 template <int NT>
 __device__ __forceinline__ float block_sum(float v, float* s) {
     v = wave_sum(v);
@@ -93,36 +93,39 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     }
     return v;
 }
-template <int NT>
-__device__ __forceinline__ uint32_t block_umax(uint32_t v, uint32_t* s) {
-    v = wave_umax(v);
-    if constexpr (NT > kWave) {
-        if ((threadIdx.x & (kWave - 1)) == 0) s[threadIdx.x / kWave] = v;
-        __syncthreads();
-        v = 0;
-#pragma unroll
-        for (int i = 0; i < NT / kWave; ++i) v = max(v, s[i]);
-    }
-    return v;
-}
-
 __device__ __forceinline__ float inverse_rms(float sum, int64_t H, float eps) {
     return 1.0f / sqrtf(sum / (float)H + eps);
 }
 
-// 8 values of y (vector v of row t) out: bf16 and codes.  Every lane of the wave calls it,
-// with `in` false past the row's end; row_scale: the rowwise format's.
+// The fp32-scaled formats encode u = h (weight + offset) under amax |u| / 448 and store that
+// times r as the scale: r is common to a row, so the codes are those of y under its own
+// scale with two roundings fewer (of y and of its maximum), and a row's largest |u| is found
+// beside its sum of squares.  Where the scale itself is 0 (r or all of u) or r is NaN, so is
+// what the codes are taken under.
+struct Scale {
+    float of_y, of_u;
+};
+__device__ __forceinline__ Scale scale_of(float top, float r) {
+    const float s = top / 448.0f, of_y = s * r;  // IEEE binary32 division
+    return {of_y, of_y == 0.0f || r != r ? of_y : s};
+}
+
+// 8 values u = h (weight + offset) (vector v of row t) out, as y = u r: bf16 and codes.  Every lane of
+// the wave calls it, with `in` false (and u 0) past the row's end; row: the rowwise format's scale.
 template <int FMT>
-__device__ __forceinline__ void put8(const NormArgs& a, int64_t t, int64_t v, bool in, const float* y,
-                                     float row_scale) {
+__device__ __forceinline__ void put8(const NormArgs& a, int64_t t, int64_t v, bool in, const float* u, float r,
+                                     const Scale& row) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = u[i] * r;
     if (in && a.y) reinterpret_cast<uint4*>(a.y + t * a.H)[v] = pack8_bf16(y);
     if constexpr (FMT == kRowwise) {
-        if (in) *reinterpret_cast<uint2*>(a.q + t * a.H + v * 8) = encode8(y, row_scale);
+        if (in) *reinterpret_cast<uint2*>(a.q + t * a.H + v * 8) = encode8(u, row.of_u);
     } else if constexpr (FMT == kBlock) {
-        const float scale = amax_of16(amax8(y)) / 448.0f;  // IEEE binary32 division
+        const Scale s = scale_of(amax_of16(amax8(u)), r);
         if (in) {
-            *reinterpret_cast<uint2*>(a.q + t * a.H + v * 8) = encode8(y, scale);
-            if ((v & 15) == 0) static_cast<float*>(a.scales)[t * ((a.H + 127) / 128) + v / 16] = scale;
+            *reinterpret_cast<uint2*>(a.q + t * a.H + v * 8) = encode8(u, s.of_u);
+            if ((v & 15) == 0) static_cast<float*>(a.scales)[t * ((a.H + 127) / 128) + v / 16] = s.of_y;
         }
     } else if constexpr (FMT == kMX) {
         // largest pattern of the block's 4 lanes: from infinity's on the block has no codes
@@ -136,6 +139,26 @@ __device__ __forceinline__ void put8(const NormArgs& a, int64_t t, int64_t v, bo
         if (in) {
             *reinterpret_cast<uint2*>(a.q + t * a.H + v * 8) = pk;
             if ((v & 3) == 0) static_cast<uint8_t*>(a.scales)[t * (a.H / 32) + v / 4] = (uint8_t)(X + 127);
+        }
+    }
+}
+
+// A row's sum of squares and, for the rowwise format, its largest |u|, over the workgroup.
+template <int NT, bool MAX>
+__device__ __forceinline__ void row_sums(float& sum, uint32_t& top, float* s_sum, uint32_t* s_top) {
+    sum = wave_sum(sum);
+    if constexpr (MAX) top = wave_umax(top);
+    if constexpr (NT > kWave) {
+        if ((threadIdx.x & (kWave - 1)) == 0) {
+            s_sum[threadIdx.x / kWave] = sum;
+            if constexpr (MAX) s_top[threadIdx.x / kWave] = top;
+        }
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT / kWave; ++i) {
+            sum += s_sum[i];
+            if constexpr (MAX) top = max(top, s_top[i]);
         }
     }
 }
@@ -178,31 +201,27 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
         }
-        if constexpr (RES) {
-#pragma unroll
-            for (int c = 0; c < VPT; ++c) {
-                const int64_t v = threadIdx.x + NT * c;
-                if (v < nv) store8<S32>(row_at<S32>(a.h, t * a.H), v, h[c]);
-            }
-        }
-        const float r = inverse_rms(block_sum<NT>(sum, s_sum[turn]), a.H, a.eps);
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < VPT; ++c) {
-            const bool in = threadIdx.x + NT * c < nv;
+            const int64_t v = threadIdx.x + NT * c;
+            if constexpr (RES)
+                if (v < nv) store8<S32>(row_at<S32>(a.h, t * a.H), v, h[c]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[c][i] = in ? h[c][i] * r * w[c][i] : 0.0f;
+            for (int i = 0; i < 8; ++i) h[c][i] = v < nv ? h[c][i] * w[c][i] : 0.0f;
             if constexpr (FMT == kRowwise) top = max(top, __float_as_uint(amax8(h[c])));
         }
-        float scale = 0.0f;
+        row_sums<NT, FMT == kRowwise>(sum, top, s_sum[turn], s_max[turn]);
+        const float r = inverse_rms(sum, a.H, a.eps);
+        Scale scale{};
         if constexpr (FMT == kRowwise) {
-            scale = __uint_as_float(block_umax<NT>(top, s_max[turn])) / 448.0f;  // IEEE binary32 division
-            if (threadIdx.x == 0) static_cast<float*>(a.scales)[t] = scale;
+            scale = scale_of(__uint_as_float(top), r);
+            if (threadIdx.x == 0) static_cast<float*>(a.scales)[t] = scale.of_y;
         }
 #pragma unroll
         for (int c = 0; c < VPT; ++c) {
             const int64_t v = threadIdx.x + NT * c;
-            put8<FMT>(a, t, v, v < nv, h[c], scale);
+            put8<FMT>(a, t, v, v < nv, h[c], r, scale);
         }
     }
 }
@@ -217,8 +236,9 @@ __global__ __launch_bounds__(NT) void rmsnorm_long_kernel(const NormArgs a) {
     int turn = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         float sum = 0.0f;
+        uint32_t top = 0;
         for (int64_t v = threadIdx.x; v < nv; v += NT) {
-            float h[8];
+            float h[8], w[8];
             load8<kX32>(row_at<kX32>(a.x, t * a.H), v, h);
             if constexpr (RES) {
                 float r[8];
@@ -230,34 +250,30 @@ __global__ __launch_bounds__(NT) void rmsnorm_long_kernel(const NormArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = fmaf(h[i], h[i], sum);
-        }
-        const float r = inverse_rms(block_sum<NT>(sum, s_sum[turn]), a.H, a.eps);
-        // a thread reads back the vectors of h that it wrote itself
-        auto value = [&](int64_t v, float* y) {
-            float w[8];
-            if (v < nv) {
-                load8<S32>(row_at<S32>(RES ? static_cast<const void*>(a.h) : a.x, t * a.H), v, y);
+            if constexpr (FMT == kRowwise) {
                 load_weight8(a, v, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+                for (int i = 0; i < 8; ++i) h[i] *= w[i];
+                top = max(top, __float_as_uint(amax8(h)));
             }
-        };
-        float scale = 0.0f, y[8];
-        if constexpr (FMT == kRowwise) {
-            uint32_t top = 0;
-            for (int64_t v = threadIdx.x; v < nv; v += NT) {
-                value(v, y);
-                top = max(top, __float_as_uint(amax8(y)));
-            }
-            scale = __uint_as_float(block_umax<NT>(top, s_max[turn])) / 448.0f;
-            if (threadIdx.x == 0) static_cast<float*>(a.scales)[t] = scale;
         }
+        row_sums<NT, FMT == kRowwise>(sum, top, s_sum[turn], s_max[turn]);
+        const float r = inverse_rms(sum, a.H, a.eps);
+        Scale scale{};
+        if constexpr (FMT == kRowwise) {
+            scale = scale_of(__uint_as_float(top), r);
+            if (threadIdx.x == 0) static_cast<float*>(a.scales)[t] = scale.of_y;
+        }
+        // a thread reads back the vectors of h that it wrote itself
         for (int64_t v = threadIdx.x; v < nv_up; v += NT) {
-            value(v, y);
-            put8<FMT>(a, t, v, v < nv, y, scale);
+            float u[8], w[8];
+            if (v < nv) {
+                load8<S32>(row_at<S32>(RES ? static_cast<const void*>(a.h) : a.x, t * a.H), v, u);
+                load_weight8(a, v, w);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = v < nv ? u[i] * w[i] : 0.0f;
+            put8<FMT>(a, t, v, v < nv, u, r, scale);
         }
     }
 }

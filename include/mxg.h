@@ -810,7 +810,7 @@ mxg_status mx_silu_backward_block128(const void* h_bf16, const void* dy_bf16, vo
  * Per row of H elements:
  *   h = x + residual, rounded to stream_type;  without a residual h = x
  *   r = 1 / sqrt(sum h^2 / H + eps)
- *   y = h * r * (weight + weight_offset)
+ *   y = h * (weight + weight_offset) * r
  *
  *   x         [num_tokens, H]: BF16 where residual is given, else of stream_type.
  *   residual  [num_tokens, H] of stream_type, or NULL.
@@ -824,7 +824,8 @@ mxg_status mx_silu_backward_block128(const void* h_bf16, const void* dy_bf16, vo
  *     MXG_NORM_MXFP8         E8M0 u8 [num_tokens, H/32], as its MXFP8,
  *     MXG_NORM_FP8_BLOCK128  fp32 [num_tokens, ceil(H/128)], as
  *                            mx_grouped_quantize_block128,
- *             of y in fp32 (no bf16 between).
+ *             of y in fp32 (no bf16 between; h * (weight + weight_offset) is formed
+ *             first, and the fp32-scaled codes are its, under its own maximum).
  * Sums and y are fp32; a row's squares are summed in a fixed order.  A row whose
  * sum of squares passes fp32's range is treated as one with an infinity: r = 0.  A row
  * or block with a NaN or infinity in y gets a non-finite scale (E8M0: 255) and in the
@@ -853,7 +854,8 @@ mxg_status mx_silu_backward_block128(const void* h_bf16, const void* dy_bf16, vo
  *
  * Errors: INVALID_VALUE for a bad type or format, H <= 0, num_tokens < 0, eps
  * negative or NaN, a null pointer that has to be given or one given that may not be
- * (h without residual, q with MXG_NORM_PLAIN, no output at all), or misalignment
+ * (h without residual, q with MXG_NORM_PLAIN, no output at all), an output that overlaps
+ * where it may not, or misalignment
  * (rows, weight and codes on 16 bytes, the rest on 4); NOT_SUPPORTED for H % 8 != 0
  * (with q: H % 32 != 0) or H or num_tokens > INT32_MAX / 2.
  * mx_rmsnorm_workspace_bytes returns -1 for sizes that the call would refuse.
@@ -923,7 +925,8 @@ mxg_status mx_rmsnorm_backward(mxg_dtype stream_type, const void* dy_bf16, const
  * total_rows, num_rows or num_groups < 0, a null pointer that has to be given, z given
  * to mx_grouped_matmul_bf16_backward with act none, mx_activation_backward with it, one
  * of row_offsets and expert_ids without the other,
- * NULL routing with num_groups or num_experts other than 1, or misalignment (16 bytes;
+ * NULL routing with num_groups or num_experts other than 1, an output that overlaps where
+ * it may not, or misalignment (16 bytes;
  * bias, dbias, row_offsets and expert_ids 4); NOT_SUPPORTED for K % 8 != 0, in the
  * gradients also N % 8 != 0, N odd with swiglu, K > MXG_MAX_K (the products' gradients: N
  * too), N > INT32_MAX / 2, total_rows or num_rows > INT32_MAX, or num_groups >
@@ -986,6 +989,18 @@ int32_t mxg_fp8_tile(int32_t num_groups, int64_t total_rows, int64_t N, int64_t 
  */
 int32_t mxg_block128_tile(int32_t num_groups, int64_t total_rows, int64_t N, int64_t K,
                           int64_t max_rows_per_group_hint);
+
+/*
+ * mxg_bf16_tile -- the same for a BF16 product (mx_grouped_matmul_bf16), its rows' gradient
+ * or its weights' gradient: 1000 * rows + columns of a tile of the kernel that runs.  256 x
+ * 256, 128 x 128 and, for the first two, 32 x 128 are tiles of the kernel that walks a list
+ * of them; 64 x 64 and, for the first two, 32 x 32 and 16 x 32, for the weights 64 x 32 are
+ * those whose depth is split over a workgroup's waves.  0 where such a call would launch
+ * nothing or be refused.
+ */
+typedef enum { MXG_BF16_FORWARD = 0, MXG_BF16_BACKWARD = 1, MXG_BF16_BACKWARD_WEIGHTS = 2 } mxg_bf16_product;
+int32_t mxg_bf16_tile(mxg_bf16_product product, int32_t num_groups, int32_t num_experts, int64_t total_rows, int64_t N,
+                      int64_t K, int64_t max_rows_per_group_hint);
 mxg_status mxg_clock_probe(unsigned long long* out, int64_t window_us, hipStream_t stream);
 
 /*
