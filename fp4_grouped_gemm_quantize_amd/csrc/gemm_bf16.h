@@ -60,13 +60,6 @@ inline int fastest(const Candidate (&c)[N], const Work& w, int64_t cus) {
     return best;
 }
 
-// The group's rows; without routing one group of all rows.
-__device__ __forceinline__ GroupRange rows_of(const uint32_t* off, const int32_t* ids, int g, int64_t T, int E) {
-    if (off == nullptr) return {0, T};
-    return group_range(off, ids, g, T, E);
-}
-__device__ __forceinline__ int expert_of(const int32_t* ids, int g) { return ids == nullptr ? 0 : ids[g]; }
-
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 // The normal distribution's Phi(z), by erfc so that it keeps its digits where it is small.
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }

@@ -97,10 +97,15 @@ struct RowsJob {
     }
 };
 
-// The routing and the M tiles before each group into LDS; returns how many tiles there are.
+// Indexes of tiles and of their halves are 32 bits wide.
+constexpr int kMostTiles = INT32_MAX / 2;
+
+// The routing and the M tiles before each group into LDS; returns how many tiles there are, N tiles and
+// all.  Rows with one owner stay below kMostTiles (the launch sees to it).  Offsets that go back need not:
+// counted in 64 bits and cut off there, the prefix never falls and each tile has its rows.
 template <class TL>
-__device__ __forceinline__ int load_groups(const Bf16Problem& p, uint32_t* s_pre, uint32_t* s_off, int32_t* s_ids,
-                                           uint32_t* s_wave) {
+__device__ __forceinline__ int load_groups(const Bf16Problem& p, int ntn, uint32_t* s_pre, uint32_t* s_off,
+                                           int32_t* s_ids, uint64_t* s_wave) {
     const int tid = threadIdx.x, G = p.G;
     if (p.off == nullptr) {  // one group
         const int total = (int)((p.T + TL::BM - 1) / TL::BM);
@@ -111,7 +116,7 @@ __device__ __forceinline__ int load_groups(const Bf16Problem& p, uint32_t* s_pre
             s_ids[0] = 0;
         }
         __syncthreads();
-        return total;
+        return total * ntn;
     }
     for (int i = tid; i <= G; i += TL::kThreads) {
         s_off[i] = p.off[i];
@@ -119,7 +124,9 @@ __device__ __forceinline__ int load_groups(const Bf16Problem& p, uint32_t* s_pre
     }
     __syncthreads();
     constexpr int kPer = (kMaxGroups + TL::kThreads - 1) / TL::kThreads;
-    uint32_t cnt[kPer], local = 0, total;
+    const uint64_t most = (uint64_t)(kMostTiles / ntn);
+    uint32_t cnt[kPer];
+    uint64_t local = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int g = tid * kPer + i;
@@ -130,62 +137,67 @@ __device__ __forceinline__ int load_groups(const Bf16Problem& p, uint32_t* s_pre
         }
         local += cnt[i];
     }
-    uint32_t before = gemm::block_exclusive_scan<TL::kThreads>(local, s_wave, &total);
+    uint64_t before = gemm::block_exclusive_scan<TL::kThreads, uint64_t>(local, s_wave, &total);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int g = tid * kPer + i;
-        if (g < G) s_pre[g] = before;
+        if (g < G) s_pre[g] = (uint32_t)(before < most ? before : most);
         before += cnt[i];
     }
-    if (tid == 0) s_pre[G] = total;
+    total = total < most ? total : most;
+    if (tid == 0) s_pre[G] = (uint32_t)total;
     __syncthreads();
-    return (int)total;
+    return __builtin_amdgcn_readfirstlane((int)total * ntn);  // in a scalar register (8192^3: 760 us without, 749)
 }
 
 template <class TL, bool BACK>
 __global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16Problem p, int ntn, int mband) {
     __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
-    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
+    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1];
+    __shared__ uint64_t s_wave[TL::kWaves];
     __shared__ int32_t s_ids[kMaxGroups];
-    const int total = load_groups<TL>(p, s_pre, s_off, s_ids, s_wave);
+    const int total = load_groups<TL>(p, ntn, s_pre, s_off, s_ids, s_wave);
     const int cols = (int)(BACK ? p.K : p.N), deep = (int)(BACK ? p.N : p.K), grid = (int)gridDim.x;
-    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, items_of(total * ntn, grid),
+    RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, mband, items_of(total, grid),
                           (int64_t)deep * 2, (int64_t)(BACK ? cols : deep) * 2, cols, deep, grid};
     run_tiles<TL>(job, s_ring, gemm::xcd_remap((int)blockIdx.x, grid), grid);
 }
 
-// Small tiles, one a workgroup, their depth split over its waves.
+// Small tiles, their depth split over a workgroup's waves.  One a workgroup: the grid has a tile for each
+// that rows with one owner make.  Offsets that go back make more, the loop's later rounds.
 template <class TL, bool BACK>
 __global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_split_kernel(const Bf16Problem p, int ntn) {
     __shared__ __attribute__((aligned(512))) uint8_t s_ring[TL::kLds];
-    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1], s_wave[TL::kWaves];
+    __shared__ uint32_t s_pre[kMaxGroups + 1], s_off[kMaxGroups + 1];
+    __shared__ uint64_t s_wave[TL::kWaves];
     __shared__ int32_t s_ids[kMaxGroups];
-    const int total = load_groups<TL>(p, s_pre, s_off, s_ids, s_wave) * ntn;
-    const int W = gemm::xcd_remap((int)blockIdx.x, (int)gridDim.x);
-    if (W >= total) return;  // workgroup-uniform
+    const int total = load_groups<TL>(p, ntn, s_pre, s_off, s_ids, s_wave), grid = (int)gridDim.x;
     const int cols = (int)(BACK ? p.K : p.N), deep = (int)(BACK ? p.N : p.K);
     RowsJob<TL, BACK> job{p, s_pre, s_off, s_ids, ntn, 1 << 20, {total, total},
                           (int64_t)deep * 2, (int64_t)(BACK ? cols : deep) * 2, cols, deep, total};
-    typename RowsJob<TL, BACK>::Coord c;
-    job.locate(W, c);
-    with_act(p.act, [&](auto act) {
-        run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
-            if constexpr (BACK) {
-                Before<8> x;
-                fetch_backward<act(), 8>(p, c.m0 + row, c.n0 + col, x);
-                finish_backward<act(), 8>(p, c.m0 + row, c.n0 + col, v, x);
-            } else {
-                Beside x;
-                if ((p.N & 7) == 0) {
-                    fetch8<act(), true>(p, c.e, c.m0 + row, c.n0 + col, x);
-                    finish8<act(), true>(p, c.m0 + row, c.n0 + col, v, x);
+    for (int64_t W = gemm::xcd_remap((int)blockIdx.x, grid); W < total; W += grid) {  // workgroup-uniform
+        typename RowsJob<TL, BACK>::Coord c;
+        job.locate((int)W, c);
+        with_act(p.act, [&](auto act) {
+            run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
+                if constexpr (BACK) {
+                    Before<8> x;
+                    fetch_backward<act(), 8>(p, c.m0 + row, c.n0 + col, x);
+                    finish_backward<act(), 8>(p, c.m0 + row, c.n0 + col, v, x);
                 } else {
-                    fetch8<act(), false>(p, c.e, c.m0 + row, c.n0 + col, x);
-                    finish8<act(), false>(p, c.m0 + row, c.n0 + col, v, x);
+                    Beside x;
+                    if ((p.N & 7) == 0) {
+                        fetch8<act(), true>(p, c.e, c.m0 + row, c.n0 + col, x);
+                        finish8<act(), true>(p, c.m0 + row, c.n0 + col, v, x);
+                    } else {
+                        fetch8<act(), false>(p, c.e, c.m0 + row, c.n0 + col, x);
+                        finish8<act(), false>(p, c.m0 + row, c.n0 + col, v, x);
+                    }
                 }
-            }
+            });
         });
-    });
+        __syncthreads();  // the sums are read before the next tile's loads take their place
+    }
 }
 
 int64_t compute_units() {
@@ -197,7 +209,7 @@ template <class TL, bool BACK>
 hipError_t launch_tile(const Bf16Problem& p, int per_cu, int mband, hipStream_t stream) {
     const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
     const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
-    if (2 * most > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
+    if (most > kMostTiles) return hipErrorInvalidValue;  // more than a device's memory holds
     const int64_t room = compute_units() * per_cu, grid = most < room ? most : room;
     hipLaunchKernelGGL((matmul_bf16_kernel<TL, BACK>), dim3((unsigned)grid), dim3(TL::kThreads), 0, stream, p,
                        (int)ntn, mband);
@@ -208,7 +220,7 @@ template <class TL, bool BACK>
 hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
     const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
     const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
-    if (most > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
+    if (most > kMostTiles) return hipErrorInvalidValue;  // more than a device's memory holds
     hipLaunchKernelGGL((matmul_bf16_split_kernel<TL, BACK>), dim3((unsigned)most), dim3(TL::kThreads), 0, stream, p,
                        (int)ntn);
     return hipGetLastError();

@@ -107,9 +107,9 @@ struct WeightsJob {
         c.rows_in = rows_left < TL::BM ? rows_left : TL::BM;
         c.cols_in = cols_left < width ? cols_left : width;
         const int first = find(c.e, 0);
-        int stages = 0;
-        for (int g = first; g >= 0; g = find(c.e, g + 1)) stages += (rows(g) + kStageDepth - 1) / kStageDepth;
-        c.stages = __builtin_amdgcn_readfirstlane(stages);
+        int64_t stages = 0;  // rows that many groups take may come to more than 32 bits
+        for (int g = first; g >= 0; g = find(c.e, g + 1)) stages += ((uint32_t)rows(g) + kStageDepth - 1) / kStageDepth;
+        c.stages = __builtin_amdgcn_readfirstlane((int)(stages < INT32_MAX / 2 ? stages : INT32_MAX / 2));
         if (first >= 0) begin(c, first);
     }
     __device__ __forceinline__ bool next(int& W, Coord& c) const {

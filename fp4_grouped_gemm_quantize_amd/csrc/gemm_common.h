@@ -82,21 +82,21 @@ __device__ __forceinline__ int xcd_remap(int b, int n) {
 }
 
 // Exclusive block-wide scan over NT threads.
-template <int NT>
-__device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s_wave, uint32_t* total) {
+template <int NT, class U = uint32_t>
+__device__ __forceinline__ U block_exclusive_scan(U v, U* s_wave, U* total) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    uint32_t inc = v;
+    U inc = v;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
-        uint32_t n = __shfl_up(inc, o, kWave);
+        U n = __shfl_up(inc, o, kWave);
         if (lane >= o) inc += n;
     }
     if (lane == kWave - 1) s_wave[wave] = inc;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    U before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < NT / kWave; ++w) {
-        uint32_t s = s_wave[w];
+        U s = s_wave[w];
         before += w < wave ? s : 0;
         all += s;
     }
