@@ -206,11 +206,11 @@ int64_t compute_units() {
 }
 
 template <class TL, bool BACK>
-hipError_t launch_tile(const Bf16Problem& p, int per_cu, int mband, hipStream_t stream) {
+hipError_t launch_tile(const Bf16Problem& p, int mband, hipStream_t stream) {
     const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
     const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
     if (most > kMostTiles) return hipErrorInvalidValue;  // more than a device's memory holds
-    const int64_t room = compute_units() * per_cu, grid = most < room ? most : room;
+    const int64_t room = compute_units(), grid = most < room ? most : room;
     hipLaunchKernelGGL((matmul_bf16_kernel<TL, BACK>), dim3((unsigned)grid), dim3(TL::kThreads), 0, stream, p,
                        (int)ntn, mband);
     return hipGetLastError();
@@ -226,16 +226,20 @@ hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Measured (us a call; 256 / 128 / 32 rows in the ring kernel, 64 / 32 / 16 with the depth split):
-// dense 8192 x 8192 of 8192: 750 / 1390 / - / -; 2048 x 2048 of 2048: 45 / 43 / 56 / 57 / 108 / 160;
-// 1024 x 1024 of 1024: 27 / 14 / 10 / 13 / 20 / 34; 256 x 4096 of 4096: 80 / 37 / 29 / 29 / 38 / 58;
-// 128 x 4096 of 7168: 105 / 59 / 42 / 25 / 38 / 49; 16 x 4096 of 7168: 101 / 55 / 41 / 20 / 13 / 19;
-// 1 x 4096 of 4096: 60 / 33 / 24 / 13 / 8.3 / 7.1; 64 x 64 of 7168: 104 / 58 / 34 / 20 / 12 / 9.3;
-// 8192 x 64 of 7168: 132 / 58 / 42 / 26 / 47 / 54; 5003 rows of 24 uneven groups, 2080 x 1000: 54 / 53 / 71 /
-// 83 / 172 / 253; the rows' gradient of 8192 x 7168 of 64: 38 / 56 / 85 / 203 / 600 / 1235.
+// Measured (us a call), the ring kernel's 256 x 256 / 256 x 128 / 128 x 128 / 64 x 128 / 32 x 128 and, with
+// the depth split, 64 x 64 / 32 x 32 / 16 x 32:
+// dense 4096 x 2048 of 2048: 47 / 37 / 51 / 66 / 98 / - / - / -; 2048 x 2048 of 2048: 45 / 30 / 24 / 33 / 50 / 57 / 108 / 160;
+// 1024 x 2048 of 2048: - / 29 / 23 / 18 / 27 / 22 / - / -; 256 x 4096 of 4096: 80 / 50 / 37 / 28 / 23 / 29 / 38 / 58;
+// 128 x 4096 of 7168: 105 / 70 / 55 / 45 / 37 / 24 / 38 / 49; 16 x 4096 of 7168: 101 / 67 / 47 / 37 / 36 / 20 / 13 / 19;
+// 1 x 4096 of 4096: 60 / 40 / 29 / 23 / 22 / 13 / 8.3 / 7.1; 64 x 64 of 7168: 104 / 68 / 45 / 39 / 34 / 20 / 12 / 9.3;
+// 5003 rows of 24 uneven groups, 2080 x 1000: 54 / 57 / 48 / 52 / 79 / 83 / 172 / 253; 512 rows of 8, 4096 x 4096:
+// - / 56 / 45 / 73 / 71 / 96 / - / -; the rows' gradient of 8192 x 7168 of 64 (256 x 256, 64 x 64 and less):
+// 38 / 203 / 600 / 1235.
+// Tiles of 128 rows and less keep four stages and more in flight: with two, 2048 x 2048 of 2048 in 128 x 128 took 43.
 constexpr Candidate kRowTiles[] = {
-    {256, 256, 1, 1, 5.0, 1.1, 12.0}, {128, 128, 1, 2, 4.0, 0.6, 11.0}, {32, 128, 1, 3, 4.0, 0.37, 11.0},
-    {64, 64, 4, 1, 3.0, 0.7, 7.5},    {32, 32, 4, 1, 3.0, 0.33, 7.5},   {16, 32, 8, 1, 4.0, 0.37, 7.5},
+    {256, 256, 1, 1, 5.0, 1.2, 12.0}, {256, 128, 1, 1, 5.0, 0.59, 12.5}, {128, 128, 1, 1, 4.5, 0.45, 14.0},
+    {64, 128, 1, 1, 4.5, 0.35, 14.5}, {32, 128, 1, 1, 3.5, 0.28, 16.0},  {64, 64, 4, 1, 3.0, 0.7, 11.0},
+    {32, 32, 4, 1, 3.0, 0.33, 7.5},   {16, 32, 8, 1, 4.0, 0.37, 7.5},
 };
 
 int row_tile(const Bf16Problem& p, bool back) {
@@ -248,11 +252,13 @@ int row_tile(const Bf16Problem& p, bool back) {
 template <bool BACK>
 hipError_t launch(const Bf16Problem& p, hipStream_t stream) {
     switch (row_tile(p, BACK)) {
-        case 0: return launch_tile<Tile<256, 256, 4, 2, false, BACK>, BACK>(p, 1, 4, stream);
-        case 1: return launch_tile<Tile<128, 128, 2, 2, false, BACK>, BACK>(p, 2, 4, stream);
-        case 2: return launch_tile<Tile<32, 128, 1, 4, false, BACK>, BACK>(p, 3, 1 << 20, stream);
-        case 3: return launch_split<SplitTile<64, 64, 4, 2, false, BACK>, BACK>(p, stream);
-        case 4: return launch_split<SplitTile<32, 32, 4, 4, false, BACK>, BACK>(p, stream);
+        case 0: return launch_tile<Tile<256, 256, 4, 2, 2, false, BACK>, BACK>(p, 4, stream);
+        case 1: return launch_tile<Tile<256, 128, 4, 2, 2, false, BACK>, BACK>(p, 4, stream);
+        case 2: return launch_tile<Tile<128, 128, 2, 4, 4, false, BACK>, BACK>(p, 4, stream);
+        case 3: return launch_tile<Tile<64, 128, 2, 4, 5, false, BACK>, BACK>(p, 1 << 20, stream);
+        case 4: return launch_tile<Tile<32, 128, 1, 4, 6, false, BACK>, BACK>(p, 1 << 20, stream);
+        case 5: return launch_split<SplitTile<64, 64, 4, 2, false, BACK>, BACK>(p, stream);
+        case 6: return launch_split<SplitTile<32, 32, 4, 4, false, BACK>, BACK>(p, stream);
         default: return launch_split<SplitTile<16, 32, 8, 3, false, BACK>, BACK>(p, stream);
     }
 }

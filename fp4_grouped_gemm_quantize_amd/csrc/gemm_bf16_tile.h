@@ -136,9 +136,10 @@ struct Operand {
 };
 
 // A tile of BM x BN outputs by WGM x WGN waves; A gives the rows, B the columns.
-template <int BM_, int BN_, int WGM_, int WGN_, bool AWIDE_, bool BWIDE_>
+template <int BM_, int BN_, int WGM_, int WGN_, int SLOTS_, bool AWIDE_, bool BWIDE_>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
+    static constexpr int kSlots = SLOTS_;  // stages in LDS
     static constexpr bool AWIDE = AWIDE_, BWIDE = BWIDE_;
     static constexpr int kWaves = WGM * WGN, kThreads = kWave * kWaves;
     static constexpr int TM = BM / WGM / 16, TN = BN / WGN / 16;  // fragments a wave
@@ -147,7 +148,7 @@ struct Tile {
     static constexpr int kStage = A::kBytes + B::kBytes;
     static constexpr int kLoads = A::kLoads + B::kLoads;
     static constexpr int kOut = 2048;  // bytes of LDS a wave's epilogue passes its results through
-    static constexpr int kLds = 2 * kStage + kWaves * kOut;
+    static constexpr int kRing = kSlots * kStage, kLds = kRing + kWaves * kOut;
     // column blocks of a stage's second step behind which the two barriers stand
     static constexpr int kRead = TN >= 8 ? 1 : 0, kLanded = TN >= 8 ? 3 : TN >= 4 ? 1 : TN - 1;
     // A stage's loads are spread over the column blocks from kRead on, about one a block: the loads'
@@ -207,14 +208,14 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     int cw = first;
     if (!job.next(cw, cc)) return;  // workgroup-uniform
 
-    // ---- the producer: two stages ahead.  Pointers, ranges, offsets and `left` (depth from its stage to
+    // ---- the producer: kSlots stages ahead.  Pointers, ranges, offsets and `left` (depth from its stage to
     // the segment's end) are those of its next stage; past the last tile `left` is 0 and its loads
     // have an empty range, so that they need no branch.
     typename Job::Coord pc = cc;
     int pw = cw, left = 0, ra = 0, rb = 0;  // ra, rb: the ranges
     uint64_t pa = 0, pb = 0;
-    uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * 1024);
-    const uint32_t slots = 2 * slot + TL::kStage;  // slot + the other slot
+    const uint32_t slot0 = (uint32_t)__builtin_amdgcn_readfirstlane(gemm::lds_addr(s_ring) + wave * 1024);
+    uint32_t slot = slot0;
     const int64_t sa = gemm::first_lane64(A::step(job.lda)), sb = gemm::first_lane64(B::step(job.ldb));
     A fa;
     B fb;
@@ -264,7 +265,8 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
         for (int l = 0; l < TL::kLoads; ++l) load(w, l);
     };
     auto advance = [&]() {  // behind a stage's loads
-        slot = slots - slot;
+        if constexpr (TL::kSlots == 2) slot = 2 * slot0 + TL::kStage - slot;
+        else slot = slot < slot0 + TL::kRing - TL::kStage ? slot + TL::kStage : slot0;
         pa += sa;
         pb += sb;
         if (left == 0) return;  // past the last tile
@@ -281,11 +283,12 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
         }
     };
     next_tile(true);
-    load_all();
-    advance();
-    load_all();
-    advance();
-    stage_barrier<TL::kLoads>();
+#pragma unroll
+    for (int i = 0; i < TL::kSlots; ++i) {
+        load_all();
+        advance();
+    }
+    stage_barrier<(TL::kSlots - 1) * TL::kLoads>();
 
     // ---- the consumer
     v8b tf[2][TM], nf[TN];
@@ -299,6 +302,18 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     // fragments' own addresses are made where they are read and hold no registers)
     uint32_t ca = gemm::lds_addr(s_ring) + abase, cb = gemm::lds_addr(s_ring) + A::kBytes + bbase;
     const uint32_t turn_a = 2 * ca + TL::kStage, turn_b = 2 * cb + TL::kStage;
+    int turn = 0;  // the present slot, where there are more than two
+    auto next_slot = [&](uint32_t& na, uint32_t& nb) {
+        if constexpr (TL::kSlots == 2) {
+            na = turn_a - ca;
+            nb = turn_b - cb;
+        } else {
+            const int by = turn + 1 < TL::kSlots ? TL::kStage : TL::kStage - TL::kRing;
+            turn = turn + 1 < TL::kSlots ? turn + 1 : 0;
+            na = ca + by;
+            nb = cb + by;
+        }
+    };
     // a stage begins with these fragments in registers, read in this order; the rest follow in it
     constexpr int kPre = TN < 3 ? TN : 3;
     auto first_frags = [&]() {
@@ -337,7 +352,8 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
             first_frags();  // (read at the end of the tile before, too: they hold no registers through its epilogue)
             for (int kt = 0; kt < stages; ++kt) {
                 const Where w = where();
-                uint32_t na = turn_a - ca, nb = turn_b - cb;
+                uint32_t na, nb;
+                next_slot(na, nb);
                 if constexpr (A::kWide) __asm__ volatile("" : "+v"(ca), "+v"(na));
                 if constexpr (B::kWide) __asm__ volatile("" : "+v"(cb), "+v"(nb));
 #pragma unroll
@@ -367,7 +383,7 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
 #pragma unroll
                         for (int q = TL::loads_before(i); q < TL::loads_before(i + 1); ++q) load(w, q);
                     if (i == TL::kLanded) {
-                        if (!ahead) gemm::wait_vmem<TL::loads_before(TL::kLanded + 1)>();
+                        if (!ahead) gemm::wait_vmem<(TL::kSlots - 2) * TL::kLoads + TL::loads_before(TL::kLanded + 1)>();
                         ahead = false;
                         read_barrier();
                     }
@@ -388,11 +404,11 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
                 ca = na;
                 cb = nb;
             }
-            // The next tile's second stage is awaited here, before the epilogue's stores: behind them its
+            // The next tile's stages are awaited here, before the epilogue's stores: behind them its
             // wait would be theirs too.
             gemm::wait_vmem<0>();
             ahead = true;
-            job.template finish<TL>(cc, acc, wm, wn, s_ring + 2 * TL::kStage + wave * TL::kOut);
+            job.template finish<TL>(cc, acc, wm, wn, s_ring + TL::kRing + wave * TL::kOut);
             if constexpr (Job::kSums)
                 if (add_up)
 #pragma unroll
@@ -407,11 +423,10 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
             for (int kt = 0; kt < stages; ++kt) {
                 read_barrier();
                 load_all();
-                stage_barrier<TL::kLoads>();
+                stage_barrier<(TL::kSlots - 1) * TL::kLoads>();
                 ahead = false;
                 advance();
-                ca = turn_a - ca;
-                cb = turn_b - cb;
+                next_slot(ca, cb);
             }
         }
         cw += step;

@@ -210,10 +210,10 @@ int64_t compute_units() {
 // Measured (us a call; 256 and 128 rows in the ring kernel, 64 x 64 and 64 x 32 with the depth split):
 // 32768 rows of 64 uneven experts, 1536 x 4096: 690 / 1220 / 2590 / 4480; 8192 rows, 4096 x 7168: 420 / 610 / 766 /
 // 1314; 16384 rows of 8, 256 x 2048: 60 / 40 / 42 / 67; 4096 rows, 512 x 1024: 98 / 50 / 18 / 17; 8192 rows,
-// 64 x 7168: 155 / 98 / 34 / 31; 5003 rows of 24, 1000 x 2080: 91 / 127 / 283 / 469.
+// 64 x 7168: 155 / 98 / 33 / 31 (operands from HBM: 75 and 69 for the last two); 5003 rows of 24, 1000 x 2080: 91 / 127 / 283 / 469.
 constexpr Candidate kWeightTiles[] = {
     {256, 256, 1, 1, 12.0, 1.1, 12.0}, {128, 128, 1, 2, 6.0, 0.6, 11.0}, {64, 64, 4, 1, 3.0, 0.95, 11.0},
-    {64, 32, 4, 1, 3.0, 0.87, 11.0},
+    {64, 32, 4, 1, 3.0, 0.87, 12.6},
 };
 
 int weight_tile(int G, int E, int64_t T, int64_t N, int64_t K) {
@@ -271,8 +271,8 @@ hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, b
     };
     auto pick = [&](auto bias) {
         switch (weight_tile(G, E, T, N, K)) {
-            case 0: return whole(Tile<256, 256, 4, 2, true, true>{}, bias, 1);
-            case 1: return whole(Tile<128, 128, 2, 2, true, true>{}, bias, 2);
+            case 0: return whole(Tile<256, 256, 4, 2, 2, true, true>{}, bias, 1);
+            case 1: return whole(Tile<128, 128, 2, 2, 2, true, true>{}, bias, 2);
             case 2: return split(SplitTile<64, 64, 4, 2, true, true>{}, bias);
             default: return split(SplitTile<64, 32, 4, 3, true, true>{}, bias);
         }

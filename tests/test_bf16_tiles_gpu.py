@@ -29,9 +29,11 @@ def routing(T, E):
     (33000, 9, 776, 72, (256, 256)),     # two stages, the second of 8; several rounds
     (40000, 4, 1032, 64, (256, 256)),    # one stage a tile
     (45000, 3, 600, 136, (256, 256)),    # a split last round
-    (4000, 5, 1000, 2080, (128, 128)),
-    (2048, 1, 2048, 200, (128, 128)), (2500, 1, 2049, 1000, (128, 128)),
-    (2048, 24, 520, 264, (32, 128)), (900, 80, 262, 1000, (32, 128)), (700, 80, 1030, 136, (32, 128)),
+    (4000, 5, 1000, 2080, (256, 128)), (2500, 1, 2049, 1000, (256, 128)), (33000, 24, 264, 72, (256, 128)),
+    (2048, 6, 1544, 520, (128, 128)), (2048, 1, 2048, 200, (128, 128)), (16640, 80, 71, 1032, (128, 128)),
+    (16640, 6, 64, 8, (128, 128)),
+    (2048, 24, 520, 264, (64, 128)), (1500, 6, 775, 264, (64, 128)), (700, 6, 1544, 4104, (64, 128)),
+    (900, 80, 262, 1000, (32, 128)), (700, 80, 1030, 136, (32, 128)),
     (1000, 1, 1024, 264, (64, 64)), (900, 1, 999, 520, (64, 64)), (120, 1, 4096, 1040, (64, 64)), (8192, 1, 60, 4104, (64, 64)),
     (17, 1, 4100, 2056, (32, 32)), (60, 1, 1030, 1000, (32, 32)),
     (1, 1, 100, 7168, (16, 32)), (33, 1, 65, 4360, (16, 32)), (5, 1, 31, 8, (32, 32)),
@@ -47,8 +49,9 @@ def test_product(T, E, N, K, tile):
 @pytest.mark.parametrize("T,E,K,N,tile", [
     (16640, 1, 520, 320, (256, 256)), (33000, 9, 776, 72, (256, 256)), (40000, 4, 1032, 64, (256, 256)),
     (45000, 3, 600, 136, (256, 256)), (8192, 1, 7168, 64, (256, 256)),
-    (4000, 5, 1000, 2080, (128, 128)), (2500, 1, 2056, 1000, (128, 128)),
-    (2048, 24, 520, 264, (32, 128)), (900, 80, 264, 1000, (32, 128)),
+    (4000, 5, 1000, 2080, (256, 128)), (2500, 1, 2056, 1000, (256, 128)), (8192, 24, 520, 8, (256, 128)),
+    (1000, 6, 2056, 72, (128, 128)), (8192, 6, 264, 2080, (128, 128)), (16640, 6, 8, 1024, (128, 128)),
+    (2048, 24, 520, 264, (64, 128)), (4100, 24, 264, 264, (64, 128)), (900, 80, 264, 1000, (32, 128)),
     (1000, 1, 1024, 264, (64, 64)), (120, 1, 4096, 1040, (64, 64)), (8192, 1, 64, 4104, (64, 64)),
     (17, 1, 4104, 2056, (32, 32)),
     (1, 1, 104, 7168, (16, 32)), (33, 1, 72, 4360, (16, 32)),
@@ -63,7 +66,7 @@ def test_rows_gradient(T, E, K, N, tile):
     (9000, 1, 4096, 1544, (256, 256)), (5000, 33, 1288, 1032, (256, 256)), (700, 80, 1024, 776, (256, 256)),
     (16000, 8, 2056, 264, (128, 128)), (8000, 20, 520, 264, (128, 128)),
     (1500, 1, 4104, 72, (64, 64)), (300, 6, 264, 264, (64, 64)), (4100, 1, 1032, 512, (64, 64)),
-    (6000, 1, 1544, 200, (64, 32)), (300, 6, 520, 72, (64, 32)), (8192, 1, 7168, 64, (64, 64)), (8192, 1, 4096, 8, (64, 32)), (3, 1, 64, 8, (64, 32)),
+    (6000, 1, 1544, 200, (64, 32)), (300, 6, 520, 72, (64, 32)), (8192, 1, 7168, 64, (64, 32)), (8192, 1, 4096, 8, (64, 32)), (3, 1, 64, 8, (64, 32)),
 ])
 def test_weights_gradient(T, E, K, N, tile):
     assert mxg.bf16_tile(WTS, E, E, T, N, K) == tile
