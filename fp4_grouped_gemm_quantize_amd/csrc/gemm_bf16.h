@@ -1,6 +1,6 @@
 // gemm_bf16.h -- what the BF16 products' kernels share: the argument block, the
-// activations with their derivatives, and the epilogues of four neighbouring columns
-// of a row.  Device code for gfx950.
+// activations with their derivatives, the epilogues of eight neighbouring columns of a
+// row, and the choice of tile.  Device code for gfx950, and that choice for the host.
 #pragma once
 
 #include "mxg_device.h"

@@ -1,6 +1,23 @@
 // gemm_bf16.hip -- ragged grouped product of BF16 operands with bias, activation and
 // residual in its epilogue, the gradient of its rows through the activation before
 // them, and the activation's gradient by itself, for gfx950.
+//
+//   z[t,n] = sum_k a[t,k] b[e,n,k] + bias[e,n],  c = act(z) + residual
+//   da[t,k] = act'(z[t,k]) sum_n dc[t,n] b[e,n,k]
+//
+// One tile list over all groups: a prefix of the groups' M tiles in LDS gives a workgroup its tiles from their
+// numbers, in bands of four M tiles with N outer, so that the workgroups of one XCD share weights and rows
+// in its L2.  Two kinds of kernel:
+//  * The ring (gemm_bf16_tile.h): one workgroup a CU walks tiles and never drains its loads.  256 x 256 for
+//    large products: 1.50 PFLOP/s at 8192^3 (740 us), where a large library product reaches 1.54; bound by the
+//    matrix cores at the clock that their power allows (1.7 GHz) and by the stages' loads and fragment reads.
+//    With SwiGLU, bias and z kept over 65536 rows of 128 uneven experts 0.95 PFLOP/s: partial tiles, and an
+//    epilogue of 9 us a tile whose stores come in bursts.
+//  * The split: tiles of 64 x 64 and less, the depth dealt to four or eight waves with a ring each and no
+//    barrier until their sums are joined, for products of few tiles: there a stage's latency bounds the time,
+//    and each wave has 1/4 or 1/8 of the stages.  128 rows by 4096 x 7168 weights 24 us (2.4 TB/s of weights;
+//    128 workgroups, each near what a CU's loads reach), 64 x 64 of 7168 9 us.
+// Which one runs is a fit to measured times, beside kRowTiles.
 #include "gemm_bf16_tile.h"
 
 namespace mxg {
@@ -228,7 +245,8 @@ hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
 
 // Measured (us a call), the ring kernel's 256 x 256 / 256 x 128 / 128 x 128 / 64 x 128 / 32 x 128 and, with
 // the depth split, 64 x 64 / 32 x 32 / 16 x 32:
-// dense 4096 x 2048 of 2048: 47 / 37 / 51 / 66 / 98 / - / - / -; 2048 x 2048 of 2048: 45 / 30 / 24 / 33 / 50 / 57 / 108 / 160;
+// dense 4096 x 2048 of 2048: 47 / 37 / 51 / 66 / 98 / - / - / -;
+// 2048 x 2048 of 2048: 45 / 30 / 24 / 33 / 50 / 57 / 108 / 160;
 // 1024 x 2048 of 2048: - / 29 / 23 / 18 / 27 / 22 / - / -; 256 x 4096 of 4096: 80 / 50 / 37 / 28 / 23 / 29 / 38 / 58;
 // 128 x 4096 of 7168: 105 / 70 / 55 / 45 / 37 / 24 / 38 / 49; 16 x 4096 of 7168: 101 / 67 / 47 / 37 / 36 / 20 / 13 / 19;
 // 1 x 4096 of 4096: 60 / 40 / 29 / 23 / 22 / 13 / 8.3 / 7.1; 64 x 64 of 7168: 104 / 68 / 45 / 39 / 34 / 20 / 12 / 9.3;

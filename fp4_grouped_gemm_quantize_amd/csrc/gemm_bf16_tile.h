@@ -1,6 +1,6 @@
 // gemm_bf16_tile.h -- the K pipeline of the BF16 products: operand stages of 64 in
-// depth through two LDS slots filled by direct global->LDS loads, read into the matrix
-// core's registers one step ahead.  Device code for gfx950.
+// depth through a ring of LDS slots filled by direct global->LDS loads, read into the
+// matrix core's registers one step ahead.  Device code for gfx950.
 //
 //  * Matrix core: v_mfma_f32_16x16x32_bf16, accumulating.  Operands trade places as in
 //    the FP8 products: the operand whose rows become the output's columns is the
@@ -16,10 +16,13 @@
 //    expert's rows, whatever they hold) takes no part.
 //  * A stage is two steps of 32 in depth.  While a step is multiplied, the next step's
 //    fragments replace its own, one by one.  Two barriers a stage: behind the first
-//    (all waves have read the slot) its slot is filled with the stage after the next;
-//    behind the second (the next stage has landed) the next stage's fragments are read.
-//    A load has about 1.3 stages to land.  The stages run on across tiles: an epilogue
-//    has the next tile's first two stages in flight behind it.
+//    (all waves have read the slot) its slot is filled with the stage that follows those
+//    in the ring; behind the second (the next stage has landed) the next stage's fragments
+//    are read.  The stages run on across tiles: an epilogue has the next tile's first
+//    stages in flight behind it.
+//  * Slots: a stage of 256 x 256 takes 1.4 us, longer than its loads, so two slots (128 KB)
+//    do.  A stage of 128 x 128 takes 0.4 us, a load up to 1.2: four slots of half the size
+//    (2048^3: 24 us against 43 with two and two workgroups a CU); 64 x 128 five, 32 x 128 six.
 #pragma once
 
 #include "gemm_bf16.h"

@@ -5,6 +5,13 @@
 // depth is their row index), so both go through the transposing LDS loads.  A tile's depth
 // is its expert's rows, group by group; the tiles of all experts are one list, so that short
 // and long ones share the chip, and a tile without rows costs its zeros alone.
+//
+// Bound by what it writes where experts have few rows (dw in fp32 is 4 N K bytes an expert: 32768 rows of 64
+// experts, 1536 x 4096, 685 us, 1.6 GB of dw at 2.4 TB/s beside 0.6 PFLOP/s: an expert's 512 rows are eight
+// stages, behind which its tile's stores wait for memory), by the transposing reads and the power where they
+// have many (8192^3 835 us, 1.32 PFLOP/s, a library product of the same layout 946).  A router's
+// weights (64 x 7168 over 8192 rows) are few tiles with a long depth: split over a workgroup's waves 31 us.
+// Experts' rows stay in one workgroup, so a repeated call gives the same bits; no atomics, no workspace.
 #include "gemm_bf16_tile.h"
 
 namespace mxg {
@@ -179,7 +186,8 @@ __global__ __launch_bounds__(TL::kThreads, 1) void weights_kernel(const WeightsA
     static_assert(TL::kLds >= 4 * kMaxGroups, "the costs fit the ring");
     if (sorted) order_experts(p, s_off, s_ids, reinterpret_cast<uint32_t*>(s_ring), s_order);
     const int grid = (int)gridDim.x;
-    WeightsJob<TL, BIAS> job{p, s_off, s_ids, sorted ? s_order : nullptr, p.N * 2, p.K * 2, items_of(p.E * p.ntn * p.ntk, grid), grid, 4};
+    WeightsJob<TL, BIAS> job{p, s_off, s_ids, sorted ? s_order : nullptr, p.N * 2, p.K * 2,
+                             items_of(p.E * p.ntn * p.ntk, grid), grid, 4};
     run_tiles<TL>(job, s_ring, gemm::xcd_remap((int)blockIdx.x, grid), grid);
 }
 
@@ -210,7 +218,8 @@ int64_t compute_units() {
 // Measured (us a call; 256 and 128 rows in the ring kernel, 64 x 64 and 64 x 32 with the depth split):
 // 32768 rows of 64 uneven experts, 1536 x 4096: 690 / 1220 / 2590 / 4480; 8192 rows, 4096 x 7168: 420 / 610 / 766 /
 // 1314; 16384 rows of 8, 256 x 2048: 60 / 40 / 42 / 67; 4096 rows, 512 x 1024: 98 / 50 / 18 / 17; 8192 rows,
-// 64 x 7168: 155 / 98 / 33 / 31 (operands from HBM: 75 and 69 for the last two); 5003 rows of 24, 1000 x 2080: 91 / 127 / 283 / 469.
+// 64 x 7168: 155 / 98 / 33 / 31 (operands from HBM: 75 and 69 for the last two);
+// 5003 rows of 24, 1000 x 2080: 91 / 127 / 283 / 469.
 constexpr Candidate kWeightTiles[] = {
     {256, 256, 1, 1, 12.0, 1.1, 12.0}, {128, 128, 1, 2, 6.0, 0.6, 11.0}, {64, 64, 4, 1, 3.0, 0.95, 11.0},
     {64, 32, 4, 1, 3.0, 0.87, 12.6},
