@@ -200,14 +200,18 @@ __global__ __launch_bounds__(TL::kThreads, 1) void weights_split_kernel(const We
     load_groups(p, s_off, s_ids);
     const int items = p.E * p.ntn * p.ntk;
     WeightsJob<TL, BIAS> job{p, s_off, s_ids, nullptr, p.N * 2, p.K * 2, {items, items}, items, 4};
-    typename WeightsJob<TL, BIAS>::Coord c;
-    job.locate(gemm::xcd_remap((int)blockIdx.x, (int)gridDim.x), c);
-    if (p.accumulate && c.stages == 0) return;
-    run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
-        Old<8> old;
-        fetch(p, c.e, c.n0 + row, c.k0 + col, old);
-        write(p, c.e, c.n0 + row, c.k0 + col, v, old);
-    });
+    const int grid = (int)gridDim.x;
+    for (int64_t W = gemm::xcd_remap((int)blockIdx.x, grid); W < items; W += grid) {  // workgroup-uniform
+        typename WeightsJob<TL, BIAS>::Coord c;
+        job.locate((int)W, c);
+        if (p.accumulate && c.stages == 0) continue;
+        run_split<TL>(job, c, s_ring, [&](int row, int col, const float* v) {
+            Old<8> old;
+            fetch(p, c.e, c.n0 + row, c.k0 + col, old);
+            write(p, c.e, c.n0 + row, c.k0 + col, v, old);
+        });
+        __syncthreads();  // the sums are read before the next tile's loads take their place
+    }
 }
 
 int64_t compute_units() {
@@ -266,8 +270,9 @@ hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, b
         using TL = decltype(tile);
         const int64_t n = tiles(TL::BM, TL::BN);
         if (n > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
-        hipLaunchKernelGGL((weights_split_kernel<TL, decltype(bias)::value>), dim3((unsigned)n), dim3(TL::kThreads), 0,
-                           stream, p);
+        const int64_t grid = n < kMostWorkgroups ? n : kMostWorkgroups;
+        hipLaunchKernelGGL((weights_split_kernel<TL, decltype(bias)::value>), dim3((unsigned)grid), dim3(TL::kThreads),
+                           0, stream, p);
         return hipGetLastError();
     };
     auto whole = [&](auto tile, auto bias, int per_cu) {

@@ -165,3 +165,62 @@ def test_rows_beside_an_overlap(N, K, hint, tile):
     c = mxg.grouped_matmul_bf16(a, b, off, ids, dtype=F32, max_rows_per_group_hint=hint)
     want, size = a[200].double() @ b[1].double().t(), a[200].double().abs() @ b[1].double().t().abs()
     assert bool(((c[200].double() - want).abs() <= (K + 8) * 2.0 ** -23 * size + 2.0 ** -24 * want.abs()).all())
+
+
+@pytest.mark.parametrize("T,N", [(260, 264), (20, 40)])
+def test_longest_depth(T, N):
+    """K (in the rows' gradient N) of 2^22, a tile's rows 8 MiB apart; what counts stands in its last 72."""
+    D, last = 1 << 22, 72
+    a, b = torch.zeros((T, D), dtype=BF, device="cuda"), torch.zeros((1, N, D), dtype=BF, device="cuda")
+    a[:, -last:], b[0, :, -last:] = rand(1, T, last), rand(2, N, last)
+    c = mxg.grouped_matmul_bf16(a, b, dtype=F32)
+    x, y = a[:, -last:].double(), b[0, :, -last:].double().t().contiguous()
+    want, size = x @ y, x.abs() @ y.abs()
+    assert bool(((c.double() - want).abs() <= (last + 8) * 2.0 ** -23 * size + 2.0 ** -24 * want.abs()).all())
+    del b
+    w = torch.zeros((1, D, N), dtype=BF, device="cuda")
+    w[0, -last:] = rand(2, N, last).t()
+    da = torch.empty((T, N), dtype=BF, device="cuda")
+    mxg.mx_grouped_matmul_bf16_backward(a, w, da)
+    bound = (last + 8) * 2.0 ** -23 * size * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    assert bool(((da.double() - want).abs() <= bound).all())
+    # the weights' gradient with rows of 2^22 of one operand, then of the other: 40 rows
+    del w, da
+    d, g = a[:min(T, 40)], rand(3, min(T, 40), 72)
+    for rows, dc in ((d, g), (g, d)):
+        dw = torch.empty((1, dc.shape[1], rows.shape[1]), device="cuda")
+        mxg.mx_grouped_matmul_bf16_backward_weights(dc, rows, dw)
+        u, v = (t[:, -last:].double() for t in (dc, rows))
+        got = dw[0, -last:, -last:].double()
+        want, size = u.t().contiguous() @ v, u.abs().t().contiguous() @ v.abs()
+        assert bool(((got - want).abs() <= 64 * 2.0 ** -23 * size + 2.0 ** -24 * want.abs()).all())
+        assert not dw[0, :-last].any() if dc is d else not dw[0, :, :-last].any()
+
+
+def test_very_many_rows():
+    T = (1 << 27) + 1000
+    a, b = torch.zeros((T, 8), dtype=BF, device="cuda"), torch.eye(8, dtype=BF, device="cuda")[None]
+    a[-1500:] = rand(1, 1500, 8)
+    assert torch.equal(mxg.grouped_matmul_bf16(a, b), a)
+    da = torch.ones_like(a)
+    mxg.mx_grouped_matmul_bf16_backward(a, b, da)
+    assert torch.equal(da, a)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weights_gradient_of_more_tiles_than_a_launch_has_workgroups(accumulate):
+    E, T = (1 << 22) + 300, 6
+    assert mxg.bf16_tile(WTS, 3, E, T, 8, 8) == (64, 32)
+    dc, a = rand(1, T, 8), rand(2, T, 8)
+    off = torch.tensor([0, 2, 4, 6], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([0, E - 1, E - 250], dtype=torch.int32, device="cuda")
+    dw, db = torch.ones((E, 8, 8), device="cuda"), torch.ones((E, 8), device="cuda")
+    mxg.mx_grouped_matmul_bf16_backward_weights(dc, a, dw, off, ids, dbias=db, accumulate=accumulate)
+    old = float(accumulate)
+    for g, e in enumerate(ids.tolist()):
+        d, x = dc[2 * g:2 * g + 2].double().t().contiguous(), a[2 * g:2 * g + 2].double()
+        want, size = d @ x + old, d.abs() @ x.abs() + old
+        assert bool(((dw[e].double() - want).abs() <= 26 * 2.0 ** -23 * size).all())
+        assert bool(((db[e].double() - d.sum(1) - old).abs() <= 26 * 2.0 ** -23 * (d.abs().sum(1) + old)).all())
+        dw[e], db[e] = old, old
+    assert bool((dw == old).all()) and bool((db == old).all())
