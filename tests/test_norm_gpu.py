@@ -286,3 +286,37 @@ def test_graph_and_streams():
         for k in eager:
             if k != "ws":
                 assert torch.equal(cap[k], eager[k]), k
+
+
+def test_rows_past_4_gib():
+    """The last rows of every operand of two bytes an element lie past 2^32 bytes; each row is its own."""
+    S, H, n = 600100, 4096, 100
+    x, res = (torch.zeros((S, H), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-n:], res[-n:] = rand(1, n, H), rand(2, n, H)
+    w = rand(3, H)
+    h, y = torch.ones_like(x), torch.ones_like(x)
+    q = torch.ones((S, H), dtype=torch.uint8, device="cuda")
+    sc = torch.ones((S, H // 128), dtype=torch.float32, device="cuda")
+    mxg.mx_rmsnorm(x, w, residual=res, h=h, y=y, form=mxg.NORM_FP8_BLOCK128, q=q, scales=sc, eps=1e-5)
+    part = [torch.empty_like(t[:n]) for t in (h, y, q, sc)]
+    mxg.mx_rmsnorm(x[-n:].clone(), w, residual=res[-n:].clone(), h=part[0], y=part[1], form=mxg.NORM_FP8_BLOCK128,
+                   q=part[2], scales=part[3], eps=1e-5)
+    for whole, tail in zip((h, y, q, sc), part):
+        assert torch.equal(whole[-n:], tail)
+        rest = whole[:-n]
+        if whole is q:  # 0 under a negative weight is -0, whose code keeps the sign
+            assert bool((rest == ((w < 0).to(torch.uint8) << 7)).all())
+        else:
+            assert torch.count_nonzero(rest) == 0
+    del y, q, sc, res
+    dw, dx = torch.empty(H, device="cuda"), torch.ones_like(x)
+    mxg.mx_rmsnorm_backward(x, h, w, dx, dweight=dw, eps=1e-5)
+    dw_tail, dx_tail = torch.empty(H, device="cuda"), torch.empty_like(x[:n])
+    mxg.mx_rmsnorm_backward(x[-n:].clone(), h[-n:].clone(), w, dx_tail, dweight=dw_tail, eps=1e-5)
+    assert torch.equal(dx[-n:], dx_tail) and torch.count_nonzero(dx[:-n]) == 0
+    hh = h[-n:].double()
+    terms = x[-n:].double() * hh / torch.sqrt((hh * hh).mean(1, keepdim=True) + 1e-5)
+    # n terms of four fp32 roundings and r's, added by workgroup and then by at most 512 partial sums
+    bound = (n + 512 + 40) * 2.0 ** -23 * terms.abs().sum(0)
+    assert bool(((dw.double() - terms.sum(0)).abs() <= bound).all())
+    assert bool(((dw_tail.double() - terms.sum(0)).abs() <= bound).all())
