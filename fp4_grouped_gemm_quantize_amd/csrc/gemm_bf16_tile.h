@@ -40,15 +40,41 @@ constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every descriptor's
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
-// A direct-to-LDS load of 16 bytes a lane (lane l to lds + 16 l) at off + soff from a buffer
-// descriptor's base; all but off in scalar registers that no vector instruction has just written.
+// Direct-to-LDS loads of 16 bytes a lane (lane l to lds + 16 l; the next load's 1 KiB follow) at off + soff from a
+// buffer descriptor's base; all but off in scalar registers.  The wait states stand here, since nothing outside
+// keeps its place before an assembly load and the compiler gives it none: five (s_mov and s_nop 3) between a vector
+// instruction's write of a scalar register and the load that reads it -- a lane read that makes the descriptor, or
+// one that brings back a spilled offset -- and one behind each write of M0.  Loads that follow each other share them
+// (1 x 4096 of 4096, 16 x 32 split: 8.8 us with five states each, 8.1 so).
 __device__ __forceinline__ void lds_load(const v4i& desc, uint32_t off, uint32_t soff, uint32_t lds) {
     __asm__ volatile(
-        "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
+        "s_mov_b32 m0, %3\n\ts_nop 3\n\t"
         "buffer_load_dwordx4 %0, %1, %2 offen lds"
         :
         : "v"(off), "s"(desc), "s"(soff), "s"(lds)
         : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load2(const v4i& desc, uint32_t off0, uint32_t off1, uint32_t soff0, uint32_t soff1,
+                                          uint32_t lds) {
+    __asm__ volatile(
+        "s_mov_b32 m0, %5\n\ts_nop 3\n\t"
+        "buffer_load_dwordx4 %0, %2, %3 offen lds\n\ts_add_u32 m0, m0, 1024\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, %4 offen lds"
+        :
+        : "v"(off0), "v"(off1), "s"(desc), "s"(soff0), "s"(soff1), "s"(lds)
+        : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void lds_load4(const v4i& desc, uint32_t off0, uint32_t off1, uint32_t off2, uint32_t off3,
+                                          uint32_t soff0, uint32_t soff1, uint32_t soff2, uint32_t soff3, uint32_t lds) {
+    __asm__ volatile(
+        "s_mov_b32 m0, %9\n\ts_nop 3\n\t"
+        "buffer_load_dwordx4 %0, %4, %5 offen lds\n\ts_add_u32 m0, m0, 1024\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %4, %6 offen lds\n\ts_add_u32 m0, m0, 1024\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %4, %7 offen lds\n\ts_add_u32 m0, m0, 1024\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %3, %4, %8 offen lds"
+        :
+        : "v"(off0), "v"(off1), "v"(off2), "v"(off3), "s"(desc), "s"(soff0), "s"(soff1), "s"(soff2), "s"(soff3), "s"(lds)
+        : "memory", "m0", "scc");
 }
 
 // One operand's stage: R rows of the output (or its columns), NW waves filling it.
@@ -103,7 +129,22 @@ struct Operand {
         else return (int)((uint32_t)real * ld - (uint32_t)(depth - left) * 2);
     }
     __device__ __forceinline__ void load(const v4i& desc, int j, uint32_t ld, uint32_t lds) const {
-        lds_load(desc, off[j % kOffs], (uint32_t)(j / kOffs * kOffs * kStep) * ld, lds + j * (NW * 1024));
+        lds_load(desc, off[j % kOffs], soff(j, ld), lds + j * (NW * 1024));
+    }
+    static __device__ __forceinline__ uint32_t soff(int j, uint32_t ld) {
+        return (uint32_t)(j / kOffs * kOffs * kStep) * ld;
+    }
+    // All of the stage, by one wave.
+    __device__ __forceinline__ void load_all(const v4i& desc, uint32_t ld, uint32_t lds) const {
+        static_assert(NW == 1 && (kLoads == 2 || kLoads % 4 == 0), "loads in twos or fours, 1 KiB apart");
+        if constexpr (kLoads == 2) {
+            lds_load2(desc, off[0], off[1 % kOffs], soff(0, ld), soff(1, ld), lds);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLoads; j += 4)
+                lds_load4(desc, off[j % kOffs], off[(j + 1) % kOffs], off[(j + 2) % kOffs], off[(j + 3) % kOffs],
+                          soff(j, ld), soff(j + 1, ld), soff(j + 2, ld), soff(j + 3, ld), lds + j * 1024);
+        }
     }
     // bytes the base moves a stage
     static __device__ __forceinline__ int64_t step(int64_t ld) { return WIDE ? kStageDepth * ld : 128; }
@@ -251,12 +292,9 @@ __device__ __forceinline__ void run_tiles(Job& job, uint8_t* s_ring, int first, 
     auto where = [&]() {
         // (scalar already; the lane reads say so where the compiler cannot tell)
         const uint64_t ua = (uint64_t)gemm::first_lane64((int64_t)pa), ub = (uint64_t)gemm::first_lane64((int64_t)pb);
-        const Where w = {
-            {(int)(uint32_t)ua, (int)(uint32_t)(ua >> 32), __builtin_amdgcn_readfirstlane(ra), 0x00020000},
-            {(int)(uint32_t)ub, (int)(uint32_t)(ub >> 32), __builtin_amdgcn_readfirstlane(rb), 0x00020000},
-            (uint32_t)__builtin_amdgcn_readfirstlane(slot)};
-        __asm__ volatile("s_nop 4");  // wait states of what a lane read wrote
-        return w;
+        return Where{{(int)(uint32_t)ua, (int)(uint32_t)(ua >> 32), __builtin_amdgcn_readfirstlane(ra), 0x00020000},
+                     {(int)(uint32_t)ub, (int)(uint32_t)(ub >> 32), __builtin_amdgcn_readfirstlane(rb), 0x00020000},
+                     (uint32_t)__builtin_amdgcn_readfirstlane(slot)};
     };
     auto load = [&](const Where& w, int l) {
         if (l < A::kLoads) fa.load(w.da, l, lda, w.slot);
@@ -571,11 +609,8 @@ __device__ __forceinline__ void run_split(const Job& job, typename Job::Coord c,
         const v4i da = {(int)(uint32_t)pa, (int)(uint32_t)(pa >> 32), ra, 0x00020000};
         const v4i db = {(int)(uint32_t)pb, (int)(uint32_t)(pb >> 32), rb, 0x00020000};
         const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(ring0 + slot_in * TL::kStage);
-        __asm__ volatile("s_nop 4");  // wait states of what the lane reads wrote
-#pragma unroll
-        for (int l = 0; l < A::kLoads; ++l) fa.load(da, l, lda, slot);
-#pragma unroll
-        for (int l = 0; l < B::kLoads; ++l) fb.load(db, l, ldb, slot + A::kBytes);
+        fa.load_all(da, lda, slot);
+        fb.load_all(db, ldb, slot + A::kBytes);
         ++issued;
         slot_in = slot_in + 1 < TL::kSlots ? slot_in + 1 : 0;
         at += TL::kWaves * kStageDepth;
