@@ -16,10 +16,6 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 enum Act { kNone = 0, kRelu = 1, kGelu = 2, kSilu = 3, kSwiglu = 4 };  // mxg_activation
 
-// A launch of more workgroups than this could pass 2^32 threads, which none may: the kernels that have a
-// workgroup a tile loop over what is left.
-constexpr int64_t kMostWorkgroups = 1 << 22;
-
 // ---------------------------------------------------------------------------
 // Host side: which kernel a product of given sizes runs, by the time that each would take.
 // A launch of n tiles runs in rounds of `per_cu` workgroups a CU; a round takes `base` us and,

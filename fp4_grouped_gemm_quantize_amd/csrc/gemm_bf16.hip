@@ -181,7 +181,7 @@ __global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_kernel(const Bf16
 }
 
 // Small tiles, their depth split over a workgroup's waves.  One a workgroup: the grid has a tile for each
-// that rows with one owner make, up to kMostWorkgroups.  Offsets that go back make more, the loop's later
+// that rows with one owner make, as far as a launch holds them.  Offsets that go back make more, the loop's later
 // rounds.
 template <class TL, bool BACK>
 __global__ __launch_bounds__(TL::kThreads, 1) void matmul_bf16_split_kernel(const Bf16Problem p, int ntn) {
@@ -239,9 +239,8 @@ hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
     const int64_t ntn = ((BACK ? p.K : p.N) + TL::BN - 1) / TL::BN;
     const int64_t groups = p.G < p.T ? p.G : p.T, most = (p.T / TL::BM + groups) * ntn;
     if (most > kMostTiles) return hipErrorInvalidValue;  // more than a device's memory holds
-    const int64_t grid = most < kMostWorkgroups ? most : kMostWorkgroups;
-    hipLaunchKernelGGL((matmul_bf16_split_kernel<TL, BACK>), dim3((unsigned)grid), dim3(TL::kThreads), 0, stream, p,
-                       (int)ntn);
+    hipLaunchKernelGGL((matmul_bf16_split_kernel<TL, BACK>), dim3(workgroups(most, TL::kThreads)), dim3(TL::kThreads),
+                       0, stream, p, (int)ntn);
     return hipGetLastError();
 }
 

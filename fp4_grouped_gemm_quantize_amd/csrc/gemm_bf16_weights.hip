@@ -270,9 +270,8 @@ hipError_t launch_matmul_bf16_weights(const void* dc, const void* a, void* dw, b
         using TL = decltype(tile);
         const int64_t n = tiles(TL::BM, TL::BN);
         if (n > INT32_MAX) return hipErrorInvalidValue;  // more than a device's memory holds
-        const int64_t grid = n < kMostWorkgroups ? n : kMostWorkgroups;
-        hipLaunchKernelGGL((weights_split_kernel<TL, decltype(bias)::value>), dim3((unsigned)grid), dim3(TL::kThreads),
-                           0, stream, p);
+        hipLaunchKernelGGL((weights_split_kernel<TL, decltype(bias)::value>), dim3(workgroups(n, TL::kThreads)),
+                           dim3(TL::kThreads), 0, stream, p);
         return hipGetLastError();
     };
     auto whole = [&](auto tile, auto bias, int per_cu) {

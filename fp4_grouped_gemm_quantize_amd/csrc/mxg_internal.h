@@ -116,6 +116,13 @@ hipError_t launch_grouped_gemm_block128(const GemmProblem& p, hipStream_t stream
 // Rows a tile of the kernel it runs for these sizes: 256, 128, 32, 16 (the row kernel), 0 (nothing).
 int block128_tile_choice(const GemmProblem& p);
 
+// Workgroups of `threads` for n units of work.  A launch holds fewer than 2^32 threads; past 2^28 of them, 512 times
+// what a device runs at once, the workgroups loop.
+inline unsigned workgroups(int64_t n, int threads) {
+    const int64_t most = (int64_t{1} << 28) / threads;
+    return (unsigned)(n < most ? n : most);
+}
+
 // The norm of a residual stream and its gradient (norm.hip).  fmt: mxg_norm_format; s32, w32: fp32 stream, weight.
 hipError_t launch_rmsnorm(int fmt, bool s32, const void* x, const void* res, bool w32, const void* w, float w_add,
                           float eps, int64_t T, int64_t H, void* h, void* y, void* q, void* scales,

@@ -5,8 +5,10 @@
 //   g = dy (w + o),  dx = dh + r g - h r^3 (sum g h) / H,  dw = sum over rows of dy h r
 //
 // Both are HBM-bound streams: a row is read once, held in registers between its sums
-// and its outputs, and written once.  A workgroup per row (64, 256 or 1024 threads by the row's
-// length, up to four vectors of 8 elements a thread), the weight in registers over all its rows.
+// and its outputs, and written once.  Forward a workgroup per row (64, 256 or 1024 threads by the row's
+// length, up to four vectors of 8 elements a thread), or per several rows where there are more than
+// 2^28 threads' worth; backward up to 512 workgroups (64 to 1024 threads, up to two vectors each) that walk the rows with
+// the weight and its gradient's sums in registers.
 // 8192 x 4096 bf16 with residual and block-128 codes 58 us (302 MB, 5.2 TB/s; the three passes of
 // separate kernels move 1.4 times as much); the gradient of 8192 x 7168 99 us (470 MB, 4.8 TB/s); 64 x
 // 7168 8.5 us, of which 5.8 on the device: the launch, one trip to memory, one barrier.
@@ -446,17 +448,16 @@ constexpr int kMaxRow = 1024 * 8 * 4;  // elements a workgroup's registers hold
 
 template <int FMT, bool S32, bool RES>
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
-    auto go = [&](auto kernel, int nt, int64_t per) {
-        const int64_t want = (a.T + per - 1) / per;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(want < (1 << 30) ? want : (1 << 30))), dim3(nt), 0, stream, a);
+    auto go = [&](auto kernel, int nt) {
+        hipLaunchKernelGGL(kernel, dim3(workgroups(a.T, nt)), dim3(nt), 0, stream, a);
         return hipGetLastError();
     };
-    if (a.H <= 512) return go(rmsnorm_kernel<64, 1, FMT, S32, RES>, 64, 1);
-    if (a.H <= 2048) return go(rmsnorm_kernel<64, 4, FMT, S32, RES>, 64, 1);
-    if (a.H <= 4096) return go(rmsnorm_kernel<256, 2, FMT, S32, RES>, 256, 1);
-    if (a.H <= 8192) return go(rmsnorm_kernel<256, 4, FMT, S32, RES>, 256, 1);
-    if (a.H <= kMaxRow) return go(rmsnorm_kernel<1024, 4, FMT, S32, RES>, 1024, 1);
-    return go(rmsnorm_long_kernel<1024, FMT, S32, RES>, 1024, 1);
+    if (a.H <= 512) return go(rmsnorm_kernel<64, 1, FMT, S32, RES>, 64);
+    if (a.H <= 2048) return go(rmsnorm_kernel<64, 4, FMT, S32, RES>, 64);
+    if (a.H <= 4096) return go(rmsnorm_kernel<256, 2, FMT, S32, RES>, 256);
+    if (a.H <= 8192) return go(rmsnorm_kernel<256, 4, FMT, S32, RES>, 256);
+    if (a.H <= kMaxRow) return go(rmsnorm_kernel<1024, 4, FMT, S32, RES>, 1024);
+    return go(rmsnorm_long_kernel<1024, FMT, S32, RES>, 1024);
 }
 
 template <int FMT>

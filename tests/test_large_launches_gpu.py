@@ -1,0 +1,93 @@
+"""Calls with more rows than a launch holds workgroups for: the kernels loop over what is left.
+
+The inputs repeat every P rows (P prime), so that every row of the large call has to have the bits of its row
+of a small call, whose P rows are one a workgroup and are compared with 64-bit arithmetic."""
+import pytest
+import torch
+
+import fp4_grouped_gemm_quantize_amd as mxg
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
+P = 1021
+
+
+def rand(seed, *shape, scale=1.0, dtype=BF):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def repeated(rows, S):
+    """[S, ...] of the P rows over and over."""
+    out = torch.empty((S, *rows.shape[1:]), dtype=rows.dtype, device="cuda")
+    whole = S // P * P
+    out[:whole].view(S // P, P, *rows.shape[1:]).copy_(rows.expand(S // P, *rows.shape))
+    out[whole:].copy_(rows[:S - whole])
+    return out
+
+
+def check_repeats(out, rows):
+    """Every row of out has the bits of its row of rows."""
+    bits = {2: torch.int16, 4: torch.int32, 1: U8}[rows.element_size()]
+    out, rows = out.view(bits), rows.view(bits)
+    S, step = out.shape[0], max(1, (1 << 28) // max(rows.numel(), 1)) * P
+    for lo in range(0, S, step):
+        part = out[lo:lo + step]
+        n = part.shape[0] // P
+        assert bool((part[:n * P].view(n, P, *rows.shape[1:]) == rows).all()), lo
+        assert torch.equal(part[n * P:], rows[:part.shape[0] - n * P]), lo
+
+
+def norm_outputs(S, H, form, residual):
+    e = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device="cuda")  # noqa: E731
+    out = dict(h=None if residual is None else e((S, H), residual.dtype),
+               y=e((S, H), BF) if form == mxg.NORM_PLAIN else None)
+    if form != mxg.NORM_PLAIN:
+        out["q"] = e((S, H), U8)
+        out["scales"] = {mxg.NORM_FP8_ROWWISE: lambda: e((S,), F32), mxg.NORM_MXFP8: lambda: e((S, H // 32), U8),
+                         mxg.NORM_FP8_BLOCK128: lambda: e((S, -(-H // 128)), F32)}[form]()
+    return out
+
+
+# workgroups of 64, 256 and 1024 threads: 2^22, 2^20 and 2^18 of them a launch
+@pytest.mark.parametrize("S,H,form,residual", [
+    ((1 << 26) + 37, 8, mxg.NORM_PLAIN, None),          # 2^32 threads at a workgroup a row
+    ((1 << 23) + 5, 32, mxg.NORM_FP8_BLOCK128, F32),
+    ((1 << 22) + 1, 520, mxg.NORM_PLAIN, BF),
+    ((1 << 20) + 19, 2080, mxg.NORM_FP8_ROWWISE, None),
+    ((1 << 20) + 3, 4128, mxg.NORM_MXFP8, None),
+    ((1 << 18) + 7, 8224, mxg.NORM_FP8_ROWWISE, BF),
+    ((1 << 18) + 7, 32800, mxg.NORM_FP8_BLOCK128, BF)])
+def test_norm(S, H, form, residual):
+    x, w = rand(1, P, H), rand(2, H, dtype=F32)
+    res = None if residual is None else rand(3, P, H, dtype=residual)
+    small = norm_outputs(P, H, form, res)
+    mxg.mx_rmsnorm(x, w, residual=res, form=form, eps=1e-5, **small)
+    # the small call itself: fp32 arithmetic is off by less than 2^-16 of y, bf16 by 2^-8, e4m3 by 2^-4 of y or
+    # 2^-10 of the scale, which here is at most the row's maximum / 448
+    h = x.double() if res is None else (small["h"] if residual == BF else x.float() + res).double()
+    y = h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-5) * w.double()
+    if form == mxg.NORM_PLAIN:
+        assert bool(((small["y"].double() - y).abs() <= (2.0 ** -8 + 2.0 ** -15) * y.abs() + 1e-38).all())
+    else:
+        block = {mxg.NORM_FP8_ROWWISE: H, mxg.NORM_MXFP8: 32, mxg.NORM_FP8_BLOCK128: 128}[form]
+        sc = small["scales"].view(P, -1)
+        sc = torch.exp2(sc.double() - 127) if form == mxg.NORM_MXFP8 else sc.double()
+        sc = sc.repeat_interleave(block, dim=1)[:, :H]
+        got = small["q"].view(torch.float8_e4m3fn).double() * sc
+        half = (2.0 ** -4 + 2.0 ** -14) * y.abs() + 2.0 ** -10 * sc
+        if form == mxg.NORM_MXFP8:  # values from 448 of the scale on, up to 2^9 of it, become 448
+            top = y.abs() > 448 * sc
+            half = torch.where(top, 2.0 ** -3 * y.abs(), half)
+        assert bool(((got - y).abs() <= half).all())
+    large = norm_outputs(S, H, form, res)
+    xs, rs = repeated(x, S), None if res is None else repeated(res, S)
+    if rs is not None:  # h in the residual's place
+        large["h"] = rs
+    mxg.mx_rmsnorm(xs, w, residual=rs, form=form, eps=1e-5, **large)
+    del xs
+    for name in ("h", "y", "q", "scales"):
+        if large.get(name) is not None:
+            check_repeats(large[name], small[name])
