@@ -424,23 +424,27 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_long_kernel(const NormGra
     }
 }
 
-// dweight: the workspace's rows added up, 64 columns a workgroup, 16 rows at a time.
+// dweight: the workspace's rows added up, 64 columns a workgroup (and 64 more each round of the launch), 16 rows at
+// a time.
 constexpr int kParts = 16;
 __global__ __launch_bounds__(kWave * kParts) void rmsnorm_dweight_kernel(const float* __restrict__ ws, int parts,
                                                                          int64_t H, float* __restrict__ dw) {
     __shared__ float s[kParts][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t col = (int64_t)blockIdx.x * kWave + lane;
-    float v = 0.0f;
-    if (col < H)
-        for (int p = wave; p < parts; p += kParts) v += ws[p * H + col];
-    s[wave][lane] = v;
-    __syncthreads();
-    if (wave == 0 && col < H) {
-        v = 0.0f;
+    for (int64_t first = (int64_t)blockIdx.x * kWave; first < H; first += (int64_t)gridDim.x * kWave) {
+        const int64_t col = first + lane;
+        float v = 0.0f;
+        if (col < H)
+            for (int p = wave; p < parts; p += kParts) v += ws[p * H + col];
+        s[wave][lane] = v;
+        __syncthreads();
+        if (wave == 0 && col < H) {
+            v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) v += s[i][lane];
-        dw[col] = v;
+            for (int i = 0; i < kParts; ++i) v += s[i][lane];
+            dw[col] = v;
+        }
+        __syncthreads();  // s is written again for the next columns
     }
 }
 
@@ -505,8 +509,8 @@ hipError_t launch_rmsnorm_backward(bool s32, const void* dy, const void* h, bool
         const hipError_t e = s32 ? pick(std::true_type{}) : pick(std::false_type{});
         if (e != hipSuccess || !dw) return e;
     }
-    hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((unsigned)((H + kWave - 1) / kWave)), dim3(kWave * kParts), 0,
-                       stream, ws, T > 0 ? parts : 0, H, dw);
+    hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3(workgroups((H + kWave - 1) / kWave, kWave * kParts)),
+                       dim3(kWave * kParts), 0, stream, ws, T > 0 ? parts : 0, H, dw);
     return hipGetLastError();
 }
 

@@ -91,3 +91,32 @@ def test_norm(S, H, form, residual):
     for name in ("h", "y", "q", "scales"):
         if large.get(name) is not None:
             check_repeats(large[name], small[name])
+
+
+@pytest.mark.parametrize("H", [1 << 24, (1 << 24) + 72, (1 << 25) + 8])
+def test_norm_gradient_of_long_rows(H):
+    """dweight of more columns than a launch takes in one round (2^24).  A thread adds up H / 1024 squares and as many
+    products, the lanes and waves 22 more terms: a row's sums, of squares and of products' magnitudes, are off by less than
+    (H / 1024 + 22) 2^-24 of themselves, r by half of that."""
+    T = 3
+    h, dy, w = rand(1, T, H), rand(2, T, H), rand(3, H, dtype=F32)
+    dx, dw = torch.zeros_like(h), torch.full((H,), 7.0, device="cuda")
+    mxg.mx_rmsnorm_backward(dy, h, w, dx, dweight=dw, eps=1e-5)
+    sums = (H / 1024 + 22 + 16) * 2.0 ** -24
+    hd, d, g = h.double(), dy.double(), dy.double() * w.double()
+    r = 1 / torch.sqrt((hd * hd).mean(1, keepdim=True) + 1e-5)
+    terms = d * hd * r
+    assert bool(((dw.double() - terms.sum(0)).abs() <= (sums + 2.0 ** -20) * terms.abs().sum(0)).all())
+    back = hd * r ** 3 * (g * hd).mean(1, keepdim=True)
+    size = (g * r).abs() + hd.abs() * r ** 3 * (g * hd).abs().mean(1, keepdim=True)
+    want = r * g - back
+    assert bool(((dx.double() - want).abs() <= (3 * sums + 2.0 ** -20) * size + 2.0 ** -8 * want.abs() + 1e-38).all())
+
+
+def test_norm_gradient_of_no_rows():
+    """Zeros, for rows of 2^30 - 8 elements (2^34 threads at 64 columns a workgroup of 1024)."""
+    H = (1 << 30) - 8
+    e = lambda *s: torch.empty(s, dtype=BF, device="cuda")  # noqa: E731
+    dw = torch.full((H,), 7.0, device="cuda")
+    mxg.mx_rmsnorm_backward(e(0, H), e(0, H), e(H), dweight=dw)
+    assert torch.count_nonzero(dw) == 0

@@ -44,6 +44,17 @@ for t, h in ((M30 - 1, 8), (1 << 26, 512), (1 << 26, 2048), (1 << 24, 4096), (1 
 CASES["norm_codes"] = lambda: norm(M30 - 1, 32, 2)
 
 
+def norm_gradient(T, H):
+    some = T > 0
+    return "mx_rmsnorm_backward", [BF16, ptr(0) if some else None, ptr(1) if some else None, F32,
+                                   ptr(2) if some else None, f32(0), f32(1e-6), None, i64(T), i64(H),
+                                   ptr(3) if some else None, None, ptr(4), ptr(5) if some else None, None]
+
+
+for t, h in ((0, M30 - 8), (1, M30 - 8), (M30 - 1, 8), (1 << 20, 1 << 20)):
+    CASES[f"norm_gradient_{t}x{h}"] = lambda t=t, h=h: norm_gradient(t, h)
+
+
 def record(name):
     """In the process of its own: (status, launches, threads of the largest)."""
     recorder = ctypes.CDLL(os.environ["MXG_TEST_RECORDER"], mode=ctypes.RTLD_GLOBAL)
