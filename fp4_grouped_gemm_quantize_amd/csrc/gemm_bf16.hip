@@ -314,8 +314,8 @@ hipError_t launch_matmul_bf16_backward(const Bf16Problem& p, hipStream_t stream)
 
 hipError_t launch_activation_backward(int act, const void* dc, const void* z, void* dz, int64_t T, int64_t N,
                                       hipStream_t stream) {
-    const int64_t units = T * N / (act == kSwiglu ? 4 : 8), blocks = (units + 255) / 256;
-    const dim3 grid((unsigned)(blocks < (1 << 24) ? blocks : (1 << 24)));
+    const int64_t units = T * N / (act == kSwiglu ? 4 : 8);
+    const dim3 grid(workgroups((units + 255) / 256, 256));
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, dc, z, dz, units);
         return hipGetLastError();

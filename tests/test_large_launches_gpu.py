@@ -120,3 +120,32 @@ def test_norm_gradient_of_no_rows():
     dw = torch.full((H,), 7.0, device="cuda")
     mxg.mx_rmsnorm_backward(e(0, H), e(0, H), e(H), dweight=dw)
     assert torch.count_nonzero(dw) == 0
+
+
+@pytest.mark.parametrize("act,S,N", [(mxg.ACT_SWIGLU, (1 << 24) + 3, 1024), (mxg.ACT_SILU, (1 << 22) + 5, 520),
+                                     (mxg.ACT_RELU, (1 << 28) + 1, 8)])
+def test_activation_gradient(act, S, N):
+    """More vectors than a launch has threads (2^28): 2^32 of them with the first, z and dz 64 GiB in one place."""
+    wide = 2 * N if act == mxg.ACT_SWIGLU else N
+    dc, z = rand(1, P, N), rand(2, P, wide, scale=3.0)
+    small = torch.zeros_like(z)
+    mxg.mx_activation_backward(act, dc, z, small)
+    g, d = z.double(), dc.double()
+    if act == mxg.ACT_RELU:
+        want = d * (g > 0)
+        size = want.abs()
+    else:
+        if act == mxg.ACT_SWIGLU:
+            g, u = g[:, 0::2], g[:, 1::2]
+        s = 1 / (1 + torch.exp(-g))
+        slope, terms = s + g * s * (1 - s), s + g.abs() * s
+        if act == mxg.ACT_SILU:
+            want, size = d * slope, d.abs() * terms
+        else:
+            want = torch.stack((d * u * slope, d * g * s), 2).flatten(1)
+            size = torch.stack(((d * u).abs() * terms, (d * g).abs()), 2).flatten(1)
+    # fp32 arithmetic of 2^-18 of the terms, rounded once
+    assert bool(((small.double() - want).abs() <= 2.0 ** -18 * size + 2.0 ** -8 * want.abs() + 1e-38).all())
+    dcs, zs = repeated(dc, S), repeated(z, S)
+    mxg.mx_activation_backward(act, dcs, zs, zs)
+    check_repeats(zs, small)

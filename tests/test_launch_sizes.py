@@ -55,6 +55,14 @@ for t, h in ((0, M30 - 8), (1, M30 - 8), (M30 - 1, 8), (1 << 20, 1 << 20)):
     CASES[f"norm_gradient_{t}x{h}"] = lambda t=t, h=h: norm_gradient(t, h)
 
 
+def activation_gradient(act, T, N):
+    return "mx_activation_backward", [act, ptr(0), ptr(1), ptr(1), i64(T), i64(N), None]
+
+
+for a, t, n in ((4, 1 << 24, 1 << 10), (4, 1 << 20, 1 << 18), (3, 1 << 25, 1 << 10), (1, TOP, 32), (2, 1, M30 - 8)):
+    CASES[f"activation_gradient_{a}_{t}x{n}"] = lambda a=a, t=t, n=n: activation_gradient(a, t, n)
+
+
 def record(name):
     """In the process of its own: (status, launches, threads of the largest)."""
     recorder = ctypes.CDLL(os.environ["MXG_TEST_RECORDER"], mode=ctypes.RTLD_GLOBAL)
