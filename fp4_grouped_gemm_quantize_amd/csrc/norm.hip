@@ -61,6 +61,17 @@ __device__ __forceinline__ void store8(void* row, int64_t v, const float* f) {
         reinterpret_cast<uint4*>(row)[v] = pack8_bf16(f);
     }
 }
+// The same of the gradient's workspace, which lies on 4 bytes (a 16-byte access needs no more of the memory path).
+typedef float f4_on4 __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ void load8_ws(const float* row, int64_t v, float* f) {
+    const f4_on4 a = reinterpret_cast<const f4_on4*>(row)[2 * v], b = reinterpret_cast<const f4_on4*>(row)[2 * v + 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+}
+__device__ __forceinline__ void store8_ws(float* row, int64_t v, const float* f) {
+    reinterpret_cast<f4_on4*>(row)[2 * v] = f4_on4{f[0], f[1], f[2], f[3]};
+    reinterpret_cast<f4_on4*>(row)[2 * v + 1] = f4_on4{f[4], f[5], f[6], f[7]};
+}
 template <bool F32>
 __device__ __forceinline__ void* row_at(void* p, int64_t e) {
     return static_cast<uint8_t*>(p) + e * (F32 ? 4 : 2);
@@ -369,7 +380,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(const NormGradArgs
 #pragma unroll
         for (int c = 0; c < VPT; ++c) {
             const int64_t v = threadIdx.x + NT * c;
-            if (v < nv) store8<true>(ga.ws + blockIdx.x * a.H, v, dw[c]);
+            if (v < nv) store8_ws(ga.ws + blockIdx.x * a.H, v, dw[c]);
         }
     }
 }
@@ -411,10 +422,10 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_long_kernel(const NormGra
                 if (t == blockIdx.x)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dw[i] = 0.0f;
-                else load8<true>(ga.ws + blockIdx.x * a.H, v, dw);
+                else load8_ws(ga.ws + blockIdx.x * a.H, v, dw);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dw[i] = fmaf(d[i], h[i] * r, dw[i]);
-                store8<true>(ga.ws + blockIdx.x * a.H, v, dw);
+                store8_ws(ga.ws + blockIdx.x * a.H, v, dw);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) dx[i] += r * (d[i] * w[i]) - h[i] * back;
