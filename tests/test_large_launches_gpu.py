@@ -149,3 +149,25 @@ def test_activation_gradient(act, S, N):
     dcs, zs = repeated(dc, S), repeated(z, S)
     mxg.mx_activation_backward(act, dcs, zs, zs)
     check_repeats(zs, small)
+
+
+@pytest.mark.parametrize("S,H,k", [((1 << 26) + 9, 8, 1), ((1 << 22) + 5, 40, 3)])
+def test_combine(S, H, k):
+    """More tokens than a launch has waves for (2^22): 2^32 threads with the first.  Every P tokens share their rows'
+    numbers and weights; the last token's last slot is dropped."""
+    y = rand(1, 4096, H)
+    rows = torch.arange(P * k, dtype=torch.int32, device="cuda").view(P, k) * 7 % 4096
+    w = rand(2, P, k, dtype=F32)
+    small = torch.zeros((P, H), dtype=BF, device="cuda")
+    mxg.mx_moe_combine(y, rows.flatten(), w.flatten(), small)
+    terms = y[rows.long()].double() * w.double().unsqueeze(2)
+    want = terms.sum(1)
+    assert bool(((small.double() - want).abs() <= k * 2.0 ** -24 * terms.abs().sum(1) * (1 + 2.0 ** -8) +
+                 2.0 ** -8 * want.abs() + 1e-38).all())
+    many = repeated(rows, S)
+    many[-1, -1] = -1
+    out = torch.full((S, H), 7.0, dtype=BF, device="cuda")
+    mxg.mx_moe_combine(y, many.flatten(), repeated(w, S).flatten(), out)
+    check_repeats(out[:-1], small)
+    last = terms[(S - 1) % P, :k - 1].sum(0)
+    assert bool(((out[-1].double() - last).abs() <= 2.0 ** -7 * terms[(S - 1) % P].abs().sum(0)).all())
