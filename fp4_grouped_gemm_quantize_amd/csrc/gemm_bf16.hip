@@ -9,7 +9,7 @@
 // numbers, in bands of four M tiles with N outer, so that the workgroups of one XCD share weights and rows
 // in its L2.  Two kinds of kernel:
 //  * The ring (gemm_bf16_tile.h): one workgroup a CU walks tiles and never drains its loads.  256 x 256 for
-//    large products: 1.50 PFLOP/s at 8192^3 (740 us), where a large library product reaches 1.54; bound by the
+//    large products: 1.48 PFLOP/s at 8192^3 (745 us), where a large library product reaches 1.54; bound by the
 //    matrix cores at the clock that their power allows (1.7 GHz) and by the stages' loads and fragment reads.
 //    With SwiGLU, bias and z kept over 65536 rows of 128 uneven experts 0.95 PFLOP/s: partial tiles, and an
 //    epilogue of 9 us a tile whose stores come in bursts.
@@ -246,14 +246,14 @@ hipError_t launch_split(const Bf16Problem& p, hipStream_t stream) {
 
 // Measured (us a call), the ring kernel's 256 x 256 / 256 x 128 / 128 x 128 / 64 x 128 / 32 x 128 and, with
 // the depth split, 64 x 64 / 32 x 32 / 16 x 32:
-// dense 4096 x 2048 of 2048: 47 / 37 / 51 / 66 / 98 / - / - / -;
-// 2048 x 2048 of 2048: 45 / 30 / 24 / 33 / 50 / 57 / 108 / 160;
-// 1024 x 2048 of 2048: - / 29 / 23 / 18 / 27 / 22 / - / -; 256 x 4096 of 4096: 80 / 50 / 37 / 28 / 23 / 29 / 38 / 58;
-// 128 x 4096 of 7168: 105 / 70 / 55 / 45 / 37 / 24 / 38 / 49; 16 x 4096 of 7168: 101 / 67 / 47 / 37 / 36 / 20 / 13 / 19;
-// 1 x 4096 of 4096: 60 / 40 / 29 / 23 / 22 / 13 / 8.3 / 7.1; 64 x 64 of 7168: 104 / 68 / 45 / 39 / 34 / 20 / 12 / 9.3;
-// 5003 rows of 24 uneven groups, 2080 x 1000: 54 / 57 / 48 / 52 / 79 / 83 / 172 / 253; 512 rows of 8, 4096 x 4096:
-// - / 56 / 45 / 73 / 71 / 96 / - / -; the rows' gradient of 8192 x 7168 of 64 (256 x 256, 64 x 64 and less):
-// 38 / 203 / 600 / 1235.
+// dense 4096 x 2048 of 2048: 52 / 39 / 54 / 76 / 104 / 104 / 207 / 315;
+// 2048 x 2048 of 2048: 47 / 32 / 26 / 35 / 52 / 58 / 109 / 162;
+// 1024 x 2048 of 2048: 46 / 29 / 23 / 19 / 27 / 28 / 51 / 82; 256 x 4096 of 4096: 81 / 52 / 38 / 29 / 24 / 28 / 38 / 59;
+// 128 x 4096 of 7168: 105 / 69 / 55 / 45 / 37 / 24 / 36 / 48; 16 x 4096 of 7168: 104 / 67 / 49 / 38 / 36 / 20 / 12 / 19;
+// 1 x 4096 of 4096: 62 / 41 / 30 / 24 / 22 / 13 / 7.9 / 6.9; 64 x 64 of 7168: 106 / 69 / 46 / 40 / 34 / 19 / 11 / 8.7;
+// 5003 rows of 24 uneven groups, 2080 x 1000: 54 / 59 / 51 / 58 / 80 / 86 / 177 / 265; 512 rows of 8, 4096 x 4096:
+// 71 / 56 / 47 / 72 / 71 / 75 / 116 / 164; the rows' gradient of 8192 x 7168 of 64: 37 / 39 / 47 / 72 / 123 / 203 / 603 /
+// 1241.
 // Tiles of 128 rows and less keep four stages and more in flight: with two, 2048 x 2048 of 2048 in 128 x 128 took 43.
 constexpr Candidate kRowTiles[] = {
     {256, 256, 1, 1, 5.0, 1.2, 12.0}, {256, 128, 1, 1, 5.0, 0.59, 12.5}, {128, 128, 1, 1, 4.5, 0.45, 14.0},

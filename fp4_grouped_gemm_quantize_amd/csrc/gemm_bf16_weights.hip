@@ -9,8 +9,9 @@
 // Bound by what it writes where experts have few rows (dw in fp32 is 4 N K bytes an expert: 32768 rows of 64
 // experts, 1536 x 4096, 685 us, 1.6 GB of dw at 2.4 TB/s beside 0.6 PFLOP/s: an expert's 512 rows are eight
 // stages, behind which its tile's stores wait for memory), by the transposing reads and the power where they
-// have many (8192^3 835 us, 1.32 PFLOP/s, a library product of the same layout 946).  A router's
-// weights (64 x 7168 over 8192 rows) are few tiles with a long depth: split over a workgroup's waves 31 us.
+// have many (8192^3 840 us, 1.31 PFLOP/s, a library product of the same layout 946).  A router's
+// weights (64 x 7168 over 8192 rows) are few tiles with a long depth: split over a workgroup's waves 31 us where the
+// caches hold the rows, 48 where each call has others.
 // Experts' rows stay in one workgroup, so a repeated call gives the same bits; no atomics, no workspace.
 #include "gemm_bf16_tile.h"
 
@@ -220,10 +221,10 @@ int64_t compute_units() {
 }
 
 // Measured (us a call; 256 and 128 rows in the ring kernel, 64 x 64 and 64 x 32 with the depth split):
-// 32768 rows of 64 uneven experts, 1536 x 4096: 690 / 1220 / 2590 / 4480; 8192 rows, 4096 x 7168: 420 / 610 / 766 /
-// 1314; 16384 rows of 8, 256 x 2048: 60 / 40 / 42 / 67; 4096 rows, 512 x 1024: 98 / 50 / 18 / 17; 8192 rows,
-// 64 x 7168: 155 / 98 / 33 / 31 (operands from HBM: 75 and 69 for the last two);
-// 5003 rows of 24, 1000 x 2080: 91 / 127 / 283 / 469.
+// 32768 rows of 64 uneven experts, 1536 x 4096: 684 / 1147 / 2629 / 4606; 8192 rows, 4096 x 7168: 443 / 698 / 767 /
+// 1333; 16384 rows of 8, 256 x 2048: 61 / 37 / 41 / 67; 4096 rows, 512 x 1024: 103 / 60 / 18 / 16; 8192 rows,
+// 64 x 7168: 164 / 110 / 33 / 31 (one call by itself behind a write of 1 GiB, its launch with it: 76 and 67 for the last
+// two); 5003 rows of 24, 1000 x 2080: 93 / 128 / 290 / 482.
 constexpr Candidate kWeightTiles[] = {
     {256, 256, 1, 1, 12.0, 1.1, 12.0}, {128, 128, 1, 2, 6.0, 0.6, 11.0}, {64, 64, 4, 1, 3.0, 0.95, 11.0},
     {64, 32, 4, 1, 3.0, 0.87, 12.6},

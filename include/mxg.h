@@ -898,8 +898,11 @@ mxg_status mx_rmsnorm_backward(mxg_dtype stream_type, const void* dy_bf16, const
  *   row_offsets, expert_ids  as in mx_grouped_matmul; both NULL with num_groups =
  *           num_experts = 1: one dense product over all rows.
  * Sums and the epilogue are fp32, c is rounded once; act sees z in fp32, whether or not
- * it is kept.  Only covered rows are written.  max_rows_per_group_hint as in
- * mx_grouped_matmul.  Operands are not rounded; a call repeated gives the same bits.
+ * it is kept.  In fp32 e^-z is infinite below z = -88.7: from there on silu and its derivative
+ * are 0 (their magnitude is less than 2^-121).  gelu, silu and swiglu of z = -infinity are NaN, and
+ * their derivatives at either infinity, as the formulas have it.  Only covered rows are written.
+ * max_rows_per_group_hint as in mx_grouped_matmul.  Operands are not rounded; a call repeated
+ * gives the same bits.
  *
  * mx_grouped_matmul_bf16_backward -- the gradient of the rows, through the
  * activation before them:
@@ -993,10 +996,10 @@ int32_t mxg_block128_tile(int32_t num_groups, int64_t total_rows, int64_t N, int
 /*
  * mxg_bf16_tile -- the same for a BF16 product (mx_grouped_matmul_bf16), its rows' gradient
  * or its weights' gradient: 1000 * rows + columns of a tile of the kernel that runs.  256 x
- * 256, 128 x 128 and, for the first two, 32 x 128 are tiles of the kernel that walks a list
- * of them; 64 x 64 and, for the first two, 32 x 32 and 16 x 32, for the weights 64 x 32 are
- * those whose depth is split over a workgroup's waves.  0 where such a call would launch
- * nothing or be refused.
+ * 256, 128 x 128 and, for the first two, 256 x 128, 64 x 128 and 32 x 128 are tiles of the
+ * kernel that walks a list of them; 64 x 64 and, for the first two, 32 x 32 and 16 x 32, for
+ * the weights 64 x 32 are those whose depth is split over a workgroup's waves.  0 where such
+ * a call would launch nothing or be refused.
  */
 typedef enum { MXG_BF16_FORWARD = 0, MXG_BF16_BACKWARD = 1, MXG_BF16_BACKWARD_WEIGHTS = 2 } mxg_bf16_product;
 int32_t mxg_bf16_tile(mxg_bf16_product product, int32_t num_groups, int32_t num_experts, int64_t total_rows, int64_t N,
